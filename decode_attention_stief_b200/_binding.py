@@ -115,6 +115,24 @@ def library() -> ctypes.CDLL:
                                                 + [vp, vp])
             lib.stief_decode_attention_noalloc.restype = _i
             lib.stief_decode_attention_noalloc.argtypes = [vp] * 7 + [_i] * 9 + [vp, vp]
+            i64 = ctypes.c_longlong
+            lib.stief_plan_workspace_bytes.restype = ctypes.c_size_t
+            lib.stief_plan_workspace_bytes.argtypes = []
+            lib.stief_plan_pages.restype = _i
+            lib.stief_plan_pages.argtypes = [vp] * 11 + [ctypes.c_size_t] + [_i] * 5 + [vp, vp]
+            lib.stief_append_shared_paged.restype = _i
+            lib.stief_append_shared_paged.argtypes = ([vp] * 4 + [_i] * 3 + [i64, i64] + [_i] * 2
+                                                      + [vp, vp])
+            lib.stief_decode_shared_workspace_bytes.restype = ctypes.c_size_t
+            lib.stief_decode_shared_workspace_bytes.argtypes = [_i] * 3
+            lib.stief_decode_shared_paged.restype = _i
+            lib.stief_decode_shared_paged.argtypes = ([vp] * 6 + [ctypes.c_size_t] + [_i] * 8
+                                                      + [ctypes.c_float, vp, vp])
+            lib.stief_expand_shared_paged.restype = _i
+            lib.stief_expand_shared_paged.argtypes = [vp] * 8 + [_i] * 9 + [vp, vp]
+            lib.stief_prefill_attention.restype = _i
+            lib.stief_prefill_attention.argtypes = ([vp] * 7 + [_i] * 8
+                                                    + [ctypes.c_float, vp, vp])
             lib.stief_read_device_status.restype = _i
             lib.stief_read_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
             lib.stief_status_string.restype = ctypes.c_char_p
@@ -830,3 +848,192 @@ def stief_compress_append_joint_v(k_new: torch.Tensor, v_new: torch.Tensor, P_K:
     _invoke("stief_compress_append_joint_v", (pk, pv, ppk, ppv, pkl, pvl, psl, B, Hkv, T, d,
                                                    rK, rV, L_max, _opt_status(dev_status),
                                                    _stream_ptr(stream),))
+
+
+def stief_plan_workspace_bytes() -> int:
+    return int(library().stief_plan_workspace_bytes())
+
+
+def plan_workspace(device="cuda") -> torch.Tensor:
+    """A zero-filled uint8 device tensor for stief_plan_pages (every call leaves it zero)."""
+    return torch.zeros(stief_plan_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def _ws(workspace):
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _opt(t, name, dtype, ndim):
+    return None if t is None else _dev(t, name, dtype, ndim)
+
+
+def _one_device(*tensors):
+    """The tensors' device must be the current one: the library launches there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensors must be on the current device (cuda:{cur}), got {t.device}")
+
+
+def stief_plan_pages(new_tokens, seq_lens, block_table, free_pages, free_count, slots, q_start,
+                     kv_start, seq_lens_out, free_count_out, workspace, page_size: int,
+                     dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Block-table entries and pool slots of a step's new tokens, on the GPU.
+
+    new_tokens, seq_lens [B]; block_table [B][max_pages] (new entries written); free_pages
+    [num_pages], a stack whose top is entry free_count[0] - 1; slots [max_tokens], q_start and
+    kv_start [B + 1], seq_lens_out [B] (each written, or None); free_count_out [1].  All int32.
+    seq_lens_out may be seq_lens and free_count_out may be free_count.
+    """
+    i32 = torch.int32
+    pn, pl = _dev(new_tokens, "new_tokens", i32, 1), _dev(seq_lens, "seq_lens", i32, 1)
+    pt, pf = _dev(block_table, "block_table", i32, 2), _dev(free_pages, "free_pages", i32, 1)
+    pc, po = _dev(free_count, "free_count", i32, 1), _dev(free_count_out, "free_count_out", i32, 1)
+    ps, pq = _opt(slots, "slots", i32, 1), _opt(q_start, "q_start", i32, 1)
+    pk, pso = _opt(kv_start, "kv_start", i32, 1), _opt(seq_lens_out, "seq_lens_out", i32, 1)
+    B = new_tokens.shape[0]
+    if seq_lens.shape[0] != B or block_table.shape[0] != B or free_count.shape[0] != 1 \
+            or free_count_out.shape[0] != 1 \
+            or any(t is not None and t.shape[0] != B + 1 for t in (q_start, kv_start)) \
+            or (seq_lens_out is not None and seq_lens_out.shape[0] != B):
+        raise ValueError("stief_plan_pages: inconsistent shapes")
+    if slots is not None and slots.shape[0] == 0:
+        raise ValueError("stief_plan_pages: slots must not be empty (pass None)")
+    _one_device(new_tokens, seq_lens, block_table, free_pages, free_count, slots, q_start, kv_start,
+                seq_lens_out, free_count_out, workspace)
+    pw, nw = _ws(workspace)
+    _invoke("stief_plan_pages", (pn, pl, pt, pf, pc, ps, pq, pk, pso, po, pw, nw, B,
+                                 free_pages.shape[0], int(page_size), block_table.shape[1],
+                                 0 if slots is None else slots.shape[0], _opt_status(dev_status),
+                                 _stream_ptr(stream)))
+
+
+def _rows(t, name):
+    """Pointer and row stride of a 2-D bf16 CUDA tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def stief_append_shared_paged(c_new, pe_new, slots, pages,
+                              dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write rows [c_new[i] | pe_new[i]] to the pool rows slots[i] (negative: skipped).
+
+    c_new [N][r] and pe_new [N][dr] bf16 (pe_new None, or with dr = 0, for rows without a
+    position part), rows contiguous, any row stride that is a multiple of 8; slots [N] int32;
+    pages [num_pages][page_size][r + dr] bf16.
+    """
+    pc, sc = _rows(c_new, "c_new")
+    N, r = c_new.shape
+    dr = 0 if pe_new is None else pe_new.shape[1]
+    pp, sp = _rows(pe_new, "pe_new") if dr else (None, 0)
+    psl = _dev(slots, "slots", torch.int32, 1)
+    ppg = _dev(pages, "pages", torch.bfloat16, 3)
+    if slots.shape[0] != N or pages.shape[2] != r + dr or (dr and pe_new.shape[0] != N):
+        raise ValueError("stief_append_shared_paged: inconsistent shapes")
+    _one_device(c_new, pe_new, slots, pages)
+    _invoke("stief_append_shared_paged", (pc, pp, psl, ppg, N, r, dr, sc, sp, pages.shape[0],
+                                          pages.shape[1], _opt_status(dev_status),
+                                          _stream_ptr(stream)))
+
+
+def stief_decode_shared_workspace_bytes(B: int, Hq: int, r: int) -> int:
+    return int(library().stief_decode_shared_workspace_bytes(B, Hq, r))
+
+
+def shared_workspace_for(B: int, Hq: int, r: int, device="cuda") -> torch.Tensor:
+    """A uint8 device tensor of stief_decode_shared_workspace_bytes(...) bytes."""
+    n = stief_decode_shared_workspace_bytes(B, Hq, r)
+    if n == 0:
+        raise ValueError("invalid sizes for the shared decode workspace")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def stief_decode_shared_paged(q, pages, block_table, seq_lens, out, workspace, max_seq_len: int,
+                              scale: float, dev_status: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """Absorbed attention of one query token a sequence over shared latent rows:
+    out_h = sum_t softmax_t(scale * q_h . row_t) c_t.
+
+    q [B][Hq][r + dr], pages [num_pages][page_size][r + dr], out [B][Hq][r] (written), bf16;
+    block_table [B][max_pages], seq_lens [B] int32; workspace from shared_workspace_for.
+    """
+    pq, ppg = _dev(q, "q", torch.bfloat16, 3), _dev(pages, "pages", torch.bfloat16, 3)
+    pt, psl = _dev(block_table, "block_table", torch.int32, 2), _dev(seq_lens, "seq_lens", torch.int32, 1)
+    po = _dev(out, "out", torch.bfloat16, 3)
+    B, Hq, w = q.shape
+    r = out.shape[2]
+    if pages.shape[2] != w or tuple(out.shape) != (B, Hq, r) or r > w or block_table.shape[0] != B \
+            or seq_lens.shape[0] != B:
+        raise ValueError("stief_decode_shared_paged: inconsistent shapes")
+    _one_device(q, pages, block_table, seq_lens, out, workspace)
+    pw, nw = _ws(workspace)
+    _invoke("stief_decode_shared_paged", (pq, ppg, pt, psl, po, pw, nw, B, Hq, r, w - r,
+                                          pages.shape[0], pages.shape[1], block_table.shape[1],
+                                          int(max_seq_len), float(scale), _opt_status(dev_status),
+                                          _stream_ptr(stream)))
+    return out
+
+
+def stief_expand_shared_paged(pages, block_table, kv_start, W_K, W_V, k, v, k_pe=None,
+                              dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Keys and values of every head from shared latent rows: sequence b's token t becomes row
+    kv_start[b] + t of k and v, k_h = c_t . W_K[h]^T, v_h = c_t . W_V[h]^T.
+
+    pages [num_pages][page_size][r + dr], W_K and W_V [H][d][r], k and v [N][H][d], k_pe [N][dr]
+    (None, or with dr = 0, for rows without a position part) bf16; block_table [B][max_pages],
+    kv_start [B + 1] int32.
+    """
+    ppg, pt = _dev(pages, "pages", torch.bfloat16, 3), _dev(block_table, "block_table", torch.int32, 2)
+    pst = _dev(kv_start, "kv_start", torch.int32, 1)
+    pwk, pwv = _dev(W_K, "W_K", torch.bfloat16, 3), _dev(W_V, "W_V", torch.bfloat16, 3)
+    pk, pv = _dev(k, "k", torch.bfloat16, 3), _dev(v, "v", torch.bfloat16, 3)
+    H, d, r = W_K.shape
+    N, B = k.shape[0], block_table.shape[0]
+    dr = pages.shape[2] - r
+    ppe = _dev(k_pe, "k_pe", torch.bfloat16, 2) if dr > 0 and k_pe is not None else None
+    if dr < 0 or tuple(W_V.shape) != (H, d, r) or tuple(k.shape) != (N, H, d) \
+            or tuple(v.shape) != (N, H, d) or kv_start.shape[0] != B + 1 \
+            or (dr > 0 and (k_pe is None or tuple(k_pe.shape) != (N, dr))):
+        raise ValueError("stief_expand_shared_paged: inconsistent shapes")
+    _one_device(pages, block_table, kv_start, W_K, W_V, k, v, k_pe)
+    _invoke("stief_expand_shared_paged", (ppg, pt, pst, pwk, pwv, pk, pv, ppe, B, N, H, d, r, dr,
+                                          pages.shape[0], pages.shape[1], block_table.shape[1],
+                                          _opt_status(dev_status), _stream_ptr(stream)))
+
+
+def stief_prefill_attention(q, k, v, q_start, kv_start, out, max_q_len: int, scale: float,
+                            k_pe=None, dev_status: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """Causal attention of ragged prompts: query i of sequence b sees keys
+    j <= i + n_k - n_q; out = softmax_j(scale * (q . k_j + q^R . k_pe_j)) v_j.
+
+    q [Nq][Hq][d + dr], k and v [Nkv][Hkv][d], k_pe [Nkv][dr] (None when dr = 0), out
+    [Nq][Hq][d] (written), bf16; q_start, kv_start [B + 1] int32.
+    """
+    pq, pk = _dev(q, "q", torch.bfloat16, 3), _dev(k, "k", torch.bfloat16, 3)
+    pv, po = _dev(v, "v", torch.bfloat16, 3), _dev(out, "out", torch.bfloat16, 3)
+    pqs, pks = _dev(q_start, "q_start", torch.int32, 1), _dev(kv_start, "kv_start", torch.int32, 1)
+    ppe = _opt(k_pe, "k_pe", torch.bfloat16, 2)
+    Nq, Hq, dq = q.shape
+    Nkv, Hkv, d = k.shape
+    dr = 0 if k_pe is None else k_pe.shape[1]
+    if tuple(v.shape) != (Nkv, Hkv, d) or dq != d + dr or tuple(out.shape) != (Nq, Hq, d) \
+            or q_start.shape[0] != kv_start.shape[0] or (k_pe is not None and k_pe.shape[0] != Nkv):
+        raise ValueError("stief_prefill_attention: inconsistent shapes")
+    _one_device(q, k, v, q_start, kv_start, out, k_pe)
+    _invoke("stief_prefill_attention", (pq, pk, pv, ppe if dr else None, pqs, pks, po,
+                                        q_start.shape[0] - 1, Hq, Hkv, d, dr, Nq, Nkv,
+                                        int(max_q_len), float(scale), _opt_status(dev_status),
+                                        _stream_ptr(stream)))
+    return out

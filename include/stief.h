@@ -531,6 +531,136 @@ STIEF_API stief_status stief_decode_attention_noalloc(
     stief_stream_t stream);
 
 /*
+ * Page planning.  Builds, on the GPU and from the requests' lengths alone, what the paged calls
+ * read: the block-table entries of the pages that new tokens need, and the pool slot of every
+ * new token.  Sequence b holds L = seq_lens[b] tokens and takes T = new_tokens[b] more (0: it
+ * rests this step); its new tokens are flat tokens q_start[b] .. q_start[b] + T - 1.
+ *   new_tokens, seq_lens : int32 [B]                    (read)
+ *   block_table : int32 [B][max_pages]                  (entries ceil(L / page_size) ..
+ *                 ceil((L + T) / page_size) - 1 are written, nothing else)
+ *   free_pages  : int32 [num_pages]   the free page ids, a stack: entries [0, *free_count)
+ *   free_count  : int32 [1]                             (both read)
+ *   slots       : int32 [max_tokens]  slot of each flat token, page * page_size + offset; -1
+ *                 for tokens of a refused sequence and from q_start[B] on.  May be NULL.
+ *   q_start     : int32 [B + 1]  prefix sums of the new tokens.  May be NULL.
+ *   kv_start    : int32 [B + 1]  prefix sums of the lengths after the step.  May be NULL.
+ *   seq_lens_out   : int32 [B]  lengths after the step; may be seq_lens itself, or NULL (the
+ *                 compress and fused calls of this library advance the lengths themselves).
+ *   free_count_out : int32 [1]  pages left; may be free_count itself.
+ *   workspace   : stief_plan_workspace_bytes() bytes, 16-byte aligned, zero-filled once; every
+ *                 call leaves it zero.  Calls that may overlap must not share it.
+ * Pages are taken from the top of the stack (entry *free_count - 1 first), in sequence order.
+ * A sequence is refused, its table entries and length left as they were, with
+ * STIEF_DEV_CAPACITY_OVERFLOW when L + T exceeds max_pages * page_size, its flat tokens pass
+ * max_tokens (if slots is given), the page of its first new token is held already but its entry
+ * is outside [0, num_pages), or the pages it needs together with those of all sequences before
+ * it (short ones included) exceed *free_count; with STIEF_DEV_BAD_LENGTH when L or T is
+ * negative or L exceeds the capacity.  A refused sequence keeps its flat tokens.  *free_count
+ * outside [0, num_pages] is taken as the nearer bound, with STIEF_DEV_BAD_LENGTH.  A page id on
+ * the stack outside [0, num_pages) is entered as it is and its tokens get slot -1.  Sums past
+ * 2^31 - 1 are held at that value.  B <= 8192; page_size, num_pages and max_pages as for paged
+ * caches with one KV head.
+ * No array that is written may overlap another argument, except as said above.  A decode of
+ * this library issued next on the stream reads no block-table entry before this call is done.
+ */
+STIEF_API size_t stief_plan_workspace_bytes(void);
+
+STIEF_API stief_status stief_plan_pages(const int32_t* new_tokens, const int32_t* seq_lens,
+                              int32_t* block_table, const int32_t* free_pages,
+                              const int32_t* free_count, int32_t* slots, int32_t* q_start,
+                              int32_t* kv_start, int32_t* seq_lens_out, int32_t* free_count_out,
+                              void* workspace, size_t workspace_bytes, int B, int num_pages,
+                              int page_size, int max_pages, int max_tokens, uint32_t* dev_status,
+                              stief_stream_t stream);
+
+/*
+ * Shared-latent attention: keys AND values of every head from one latent vector a token.  A
+ * token's cache row is
+ *     [ c_t (r values) | k^R_t (dr values) ]     bf16, r + dr values
+ * with k_th = [ c_t . W_K[h]^T | k^R_t ] and v_th = c_t . W_V[h]^T: the latent c_t is shared by
+ * the heads and by keys and values, the position part k^R_t by the heads' keys.  It is the
+ * joint decomposition of the value heads above taken over the keys too.  The rows live in a
+ * page pool, bf16 [num_pages][page_size][r + dr], with the block tables of the paged calls
+ * (page_size a multiple of 64, num_pages * page_size < 2^31); a contiguous cache is a pool of
+ * one page a sequence.  16 <= r <= 512, 0 <= dr <= 64, both multiples of 16; up to 256 query
+ * heads.  `scale` multiplies the scores (finite).
+ *
+ * stief_append_shared_paged writes N new rows into the pool:
+ *     pages row slots[i] = [ c_new[i] | pe_new[i] ]
+ *   c_new  : bf16, row i at c_new + i * c_stride (elements; a multiple of 8, >= r)
+ *   pe_new : bf16, row i at pe_new + i * pe_stride, >= dr (NULL if dr == 0)
+ *   slots  : int32 [N]; a negative slot skips its row, one past the pool too, with
+ *            STIEF_DEV_CAPACITY_OVERFLOW.  Slots must be distinct: the row of a slot given
+ *            twice is a mixture.
+ */
+STIEF_API stief_status stief_append_shared_paged(const uint16_t* c_new, const uint16_t* pe_new,
+                              const int32_t* slots, uint16_t* pages, int N, int r, int dr,
+                              int64_t c_stride, int64_t pe_stride, int num_pages, int page_size,
+                              uint32_t* dev_status, stief_stream_t stream);
+
+/*
+ * stief_decode_shared_paged -- the absorbed form, one query token a sequence.  The caller has
+ * folded W_K into the query and folds W_V into the output projection:
+ *     q   : bf16 [B][Hq][r + dr]   (q_h . W_K[h] and the position part)
+ *     out : bf16 [B][Hq][r],  out_h = sum_t softmax_t(scale * q_h . row_t) c_t
+ * over tokens [0, seq_lens[b]).  A sequence of length 0 gives zeros; a length that is negative
+ * or above max_seq_len gives zeros and STIEF_DEV_BAD_LENGTH.  Rows at and past the length may
+ * hold anything.  Pages that are not mapped read as zeros, as in the paged decode.
+ * max_seq_len <= max_pages * page_size.  workspace: stief_decode_shared_workspace_bytes(B, Hq, r)
+ * bytes, 16-byte aligned; its contents do not matter before or after a call, but calls that may
+ * overlap must not share it.
+ * Products are bf16 on the tensor cores with fp32 sums; the weights enter the second product
+ * rounded to bf16 (a relative error of at most 2^-8 each).
+ */
+STIEF_API size_t stief_decode_shared_workspace_bytes(int B, int Hq, int r);
+
+STIEF_API stief_status stief_decode_shared_paged(const uint16_t* q, const uint16_t* pages,
+                              const int32_t* block_table, const int32_t* seq_lens, uint16_t* out,
+                              void* workspace, size_t workspace_bytes, int B, int Hq, int r, int dr,
+                              int num_pages, int page_size, int max_pages, int max_seq_len,
+                              float scale, uint32_t* dev_status, stief_stream_t stream);
+
+/*
+ * stief_expand_shared_paged -- the expanded form: keys and values of every head, for a prompt's
+ * attention.  Sequence b's tokens [0, kv_start[b + 1] - kv_start[b]) become rows
+ * kv_start[b] + t of
+ *     k, v : bf16 [N][H][d],  k_h = c_t . W_K[h]^T,  v_h = c_t . W_V[h]^T
+ *     k_pe : bf16 [N][dr]     (NULL if dr == 0)
+ *     W_K, W_V : bf16 [H][d][r]
+ * (fp32 sums, one rounding).  kv_start : int32 [B + 1], kv_start[0] == 0, ascending; rows at and
+ * past kv_start[B] are left as they were, as are rows past N, and STIEF_DEV_BAD_LENGTH is set if
+ * kv_start[B] > N.  Unmapped pages read as zeros.  d == 128.
+ */
+STIEF_API stief_status stief_expand_shared_paged(const uint16_t* pages, const int32_t* block_table,
+                              const int32_t* kv_start, const uint16_t* W_K, const uint16_t* W_V,
+                              uint16_t* k, uint16_t* v, uint16_t* k_pe, int B, int N, int H, int d,
+                              int r, int dr, int num_pages, int page_size, int max_pages,
+                              uint32_t* dev_status, stief_stream_t stream);
+
+/*
+ * stief_prefill_attention -- causal attention of ragged prompts (or prompt chunks) over
+ * per-head keys and values, those of stief_expand_shared_paged or any others.  Sequence b has
+ * n_q = q_start[b + 1] - q_start[b] queries, rows q_start[b] + i, and
+ * n_k = kv_start[b + 1] - kv_start[b] keys; query i sees keys j <= i + n_k - n_q (the last query
+ * sees them all).  A query that sees no key gives zeros.
+ *     q    : bf16 [Nq][Hq][d + dr]
+ *     k, v : bf16 [Nkv][Hkv][d]     query head h reads head h / (Hq / Hkv)
+ *     k_pe : bf16 [Nkv][dr]         shared by the heads (NULL if dr == 0)
+ *     out  : bf16 [Nq][Hq][d],  softmax_j(scale * (q . k_j + q^R . k_pe_j)) v_j
+ * q_start, kv_start : int32 [B + 1].  A sequence whose rows are not within [0, Nq) and
+ * [0, Nkv), or with more than max_q_len queries, is skipped with STIEF_DEV_BAD_LENGTH.  Output
+ * rows of no sequence are left as they were.  d == 128, 0 <= dr <= 64 a multiple of 16,
+ * Hq <= 256.  The weights enter the second product rounded to bf16.  Rows of no sequence, or of
+ * another one, may hold anything; a value row of the sequence itself that is not finite may also
+ * reach queries of the same sequence that do not see it (as a weight of 0).
+ */
+STIEF_API stief_status stief_prefill_attention(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                              const uint16_t* k_pe, const int32_t* q_start, const int32_t* kv_start,
+                              uint16_t* out, int B, int Hq, int Hkv, int d, int dr, int Nq, int Nkv,
+                              int max_q_len, float scale, uint32_t* dev_status,
+                              stief_stream_t stream);
+
+/*
  * stief_read_device_status -- synchronises `stream`, copies the device status
  * word to *value, and returns STIEF_OK if it is zero, STIEF_ERR_DEVICE_STATUS
  * if not, STIEF_ERR_CUDA if the copy failed, STIEF_ERR_INVALID_ARG for NULLs.
