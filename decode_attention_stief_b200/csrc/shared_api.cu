@@ -133,6 +133,8 @@ stief_status stief_decode_shared_paged(const uint16_t* q, const uint16_t* pages,
   stief_status st = check_pool(num_pages, page_size, max_pages);
   if (st != STIEF_OK) return st;
   if (max_seq_len > (long long)max_pages * page_size) return STIEF_ERR_CAPACITY;
+  // the work list counts 64-token tiles in 32 bits
+  if ((long long)B * ((max_seq_len + 63LL) / 64) >= (1LL << 30)) return STIEF_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(pages) || !aligned16(out) || !aligned16(workspace) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4))
     return STIEF_ERR_ALIGNMENT;

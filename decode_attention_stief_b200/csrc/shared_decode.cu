@@ -1,69 +1,592 @@
 // shared_decode.cu -- absorbed attention of one query token a sequence over a cache of shared
 // latent rows, for sm_100a.
 //
-// Every head's keys and values come from one row a token, c_t (r values) and k^R_t (dr values):
+// Every head's keys and values come from one row a token, [c_t (r values) | k^R_t (dr values)]:
 // with the key and value maps folded into the query and the output projection (the absorbed
 // form), head h computes
 //     s_t = scale * q~_h . [c_t | k^R_t],   p = softmax(s),   o~_h = sum_t p_t c_t.
-// This kernel: one CTA a (head, sequence), tiles of 64 tokens, an online softmax in fp32.
+//
+// What bounds it: the cache rows, 2 (r + dr) bytes a token, read once for all heads; at 128
+// heads the products (2 (2 r + dr) a head and token) take as long on the tensor cores.
+//
+// Both products run on tcgen05 from the same shared-memory tile of 64 rows, which TMA brings in
+// once: with the tile's rows in 128-byte swizzled atoms of 64 columns,
+//     S [64 heads x 64 tokens]   = Q~ . tile^T        (tile K-major: k = row columns)
+//     O~^T [128 dims x heads]   += tile^T . P^T       (tile MN-major: m = columns, k = tokens)
+// Keeping O~ transposed makes the accumulator r / 128 tiles of one column a head: at 64 heads
+// and r = 512 it takes 256 TMEM columns, half of the SM's, and the heads are the MMA's N, so
+// few heads cost few cycles.  More than 64 heads are split over CTAs that run side by side and
+// read the tiles through L2.
+//   warp 0: TMA producer; warp 1: MMA issuer (it also zeroes the rows past the length in a
+//   sequence's last tile: they may hold NaN, and 0 * NaN is NaN); warps 4-7: softmax, rescaling
+//   and the output.  S(i + 1) is issued before O(i), so the tensor cores work during softmax(i).
+// The running maximum is a reference that only moves when a score passes it by more than 2^8:
+// the accumulator is then rescaled in TMEM (rare); weights are at most 2^8 and rounded to bf16
+// once, and the sum l adds the rounded weights, so that a weight's rounding cancels where it
+// dominates.
+//
+// Work: the 64-token tiles of all sequences, in order, are dealt out evenly: CTA c takes tiles
+// [c per, (c + 1) per), so ragged batches and single long sequences fill the GPU alike.  A
+// sequence inside one CTA is finished there; the others leave (o~, m, l) in fp32 for a second
+// kernel, launched as a programmatic dependent, which also writes the zeros of empty sequences.
 #include <cstdint>
 
 #include "shared_latent.h"
 #include "stief_device.cuh"
+#include "umma.cuh"
 
 namespace stief {
 
 namespace {
-constexpr int kTok = 64;
+
+constexpr int kTok = 64;            // tokens per tile
+constexpr int kAtom = kTok * 128;   // bytes of one 64-column atom of a tile
+constexpr int kMaxHeads = 64;       // heads per CTA
+constexpr int kMaxStages = 8;
+constexpr int kThreads = 256;
+constexpr int kSoftWarps = 4;       // warps 4..7, one per TMEM lane quadrant
+constexpr int kMaxCtas = 160;       // the workspace holds two partial states for each
+constexpr int kMinTiles = 2;        // tiles per CTA at least (fewer would only add merging)
+constexpr uint32_t kSCol = 256;     // TMEM: O~^T at 0, S buffers at 256 and 320
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescale = 8.f;     // log2 units the reference may lag behind
+
+struct Args {
+  CUtensorMap mq;     // q [B * Hq][w], box 64 x heads
+  CUtensorMap mc;     // pool [rows][w], box 64 x 64
+  SharedDecodeArgs a;
+  int w, na, sa, nm;  // row width, atoms loaded and atoms kept a tile, 128-dim tiles of o~
+  int NH, groups, G;  // heads per CTA (a multiple of 16), head groups, CTAs per group
+  int nstage;
+  float scale2;       // scale * log2(e)
+};
+
+struct Layout {
+  uint32_t stages, p, ml, bars, total;
+};
+__host__ __device__ inline Layout layout_of(int na, int sa, int NH, int nstage) {
+  Layout l;
+  l.stages = (uint32_t)na * NH * 128;  // q~ comes first
+  l.p = l.stages + (uint32_t)nstage * sa * kAtom;
+  l.ml = l.p + (uint32_t)NH * 128;
+  l.bars = l.ml + 3 * kMaxHeads * 4;
+  l.total = l.bars + 8 * (2 * kMaxStages + 8) + 64;
+  return l;
 }
 
-__global__ void __launch_bounds__(256) stief_shared_decode_kernel(const SharedDecodeArgs a) {
-  __shared__ float qf[576], s[kTok];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int w = a.r + a.dr;
-  int L = a.seq_lens[b];
-  if (L < 0 || L > a.max_seq_len) {
-    if (tid == 0 && h == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
-    L = 0;
+// Workspace: meta int2 [B] (padded to 256 bytes), (m, l) [slots][kMaxHeads], o~ [slots][NH][r].
+__host__ __device__ inline size_t meta_bytes(int B) { return ((size_t)B * 8 + 255) / 256 * 256; }
+__host__ __device__ inline size_t ml_bytes() { return (size_t)kMaxCtas * 2 * kMaxHeads * 8; }
+
+__host__ __device__ inline int heads_per_cta(int Hq) {
+  const int g = (Hq + kMaxHeads - 1) / kMaxHeads;
+  return ((Hq + g - 1) / g + 15) / 16 * 16;
+}
+
+__device__ __forceinline__ int valid_length(int L, int most) { return L < 0 || L > most ? 0 : L; }
+
+// The stretch of one sequence's tiles [t0, t1) that a CTA works on.
+struct Segment {
+  int b, t0, t1, L;
+  bool first;  // the CTA's first
+};
+// Walks the CTA's tiles sequence by sequence; every warp role walks the same way.
+struct Walk {
+  const int32_t* lens;
+  int most, B, b, off, left;
+  bool first = true;
+  __device__ bool next(Segment& s) {
+    while (left > 0 && b < B) {
+      const int L = valid_length(__ldg(lens + b), most), n = (L + kTok - 1) / kTok;
+      if (off >= n) {
+        off = 0;
+        ++b;
+        continue;
+      }
+      s.b = b;
+      s.L = L;
+      s.t0 = off;
+      s.t1 = min(n, off + left);
+      s.first = first;
+      first = false;
+      left -= s.t1 - s.t0;
+      ++b;
+      off = 0;
+      return true;
+    }
+    return false;
   }
-  for (int i = tid; i < w; i += 256) qf[i] = bf16_to_f32(a.q[((size_t)b * a.Hq + h) * w + i]) * a.scale;
+};
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const __grid_constant__ Args p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int warp_sum[8], start_b, start_off;
+  const SharedDecodeArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = (int)blockIdx.x % p.groups, cta = (int)blockIdx.x / p.groups;
+  const int h_base = group * p.NH, nheads = min(p.NH, a.Hq - h_base);
+  const Layout lay = layout_of(p.na, p.sa, p.NH, p.nstage);
+  float* sm_f = reinterpret_cast<float*>(smem + lay.ml);  // rescale factors
+  float* sm_m = sm_f + kMaxHeads;
+  float* sm_l = sm_m + kMaxHeads;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars);  // [stages] the tile landed
+  uint64_t* empty = full + kMaxStages;   // [stages] both products have read it
+  uint64_t* q_full = empty + kMaxStages;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_full + 2;         // [2] S of a tile is in TMEM
+  uint64_t* p_full = q_full + 4;         // P of a tile is in shared memory
+  uint64_t* pv_done = q_full + 5;        // O~ of a tile is added: P and O~ are free
+  uint64_t* o_free = q_full + 6;         // the segment's O~ has been read
+  uint64_t* drain = q_full + 7;
+
+  if ((smem_u32(smem) & 1023u) != 0) {  // swizzled operands need 1 KiB alignment
+    if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(p_full, kSoftWarps);
+    mbar_init(pv_done, 1);
+    mbar_init(o_free, kSoftWarps);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    prefetch_tensormap(&p.mq);
+    prefetch_tensormap(&p.mc);
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
+
+  pdl_wait();
+  pdl_launch_dependents();
+  // where this CTA's tiles begin: a prefix sum of the sequences' tile counts
+  const int per_thread = (a.B + kThreads - 1) / kThreads, c0 = tid * per_thread, c1 = min(a.B, c0 + per_thread);
+  int sum = 0;
+  for (int b = c0; b < c1; ++b) {
+    const int L = __ldg(a.seq_lens + b);
+    if (valid_length(L, a.max_seq_len) != L && blockIdx.x == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
+    sum += (valid_length(L, a.max_seq_len) + kTok - 1) / kTok;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  tc_fence_before();
   __syncthreads();
-  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-  for (int t0 = 0; t0 < L; t0 += kTok) {
-    const int page = a.block_table[(size_t)b * a.max_pages + t0 / a.page_size];
-    const bool mapped = page >= 0 && page < a.num_pages;
-    const uint16_t* rows = a.pages + ((size_t)(mapped ? page : 0) * a.page_size + t0 % a.page_size) * w;
-    const int n = min(kTok, L - t0);
-    for (int t = warp; t < n; t += 8) {
-      float d = 0.f;
-      for (int i = lane; i < w; i += 32) d += qf[i] * (mapped ? bf16_to_f32(rows[(size_t)t * w + i]) : 0.f);
-      for (int k = 16; k; k >>= 1) d += __shfl_xor_sync(~0u, d, k);
-      if (lane == 0) s[t] = d;
-    }
-    __syncthreads();
-    float mt = m;
-    for (int t = 0; t < n; ++t) mt = fmaxf(mt, s[t]);
-    const float f = m == mt ? 1.f : __expf(m - mt);
-    l *= f, o[0] *= f, o[1] *= f;
-    m = mt;
-    for (int t = 0; t < n; ++t) {
-      const float p = __expf(s[t] - m);
-      l += p;
-      for (int j = 0; j < 2; ++j)
-        if (tid + 256 * j < a.r && mapped) o[j] += p * bf16_to_f32(rows[(size_t)t * w + tid + 256 * j]);
-    }
-    __syncthreads();
+  tc_fence_after();
+  int total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i == warp) incl += total;
+    total += warp_sum[i];
   }
-  for (int j = 0; j < 2; ++j)
-    if (tid + 256 * j < a.r)
-      a.out[((size_t)b * a.Hq + h) * a.r + tid + 256 * j] = f32_to_bf16_rn(L > 0 ? o[j] / l : 0.f);
+  int per = (total + p.G - 1) / p.G;
+  if (per < kMinTiles) per = kMinTiles;
+  const long long g0 = (long long)cta * per;
+  const int count = g0 >= total ? 0 : (int)min((long long)per, total - g0);
+  if (count > 0 && g0 >= incl - sum && g0 < incl) {  // one thread's sequences hold the first tile
+    int at = incl - sum, b = c0;
+    for (;; ++b) {
+      const int n = (valid_length(__ldg(a.seq_lens + b), a.max_seq_len) + kTok - 1) / kTok;
+      if (g0 < at + n) break;
+      at += n;
+    }
+    start_b = b;
+    start_off = (int)(g0 - at);
+  }
+  __syncthreads();
+  const uint32_t tmem = tmem_slot;
+  Walk walk{a.seq_lens, a.max_seq_len, a.B, count > 0 ? start_b : 0, count > 0 ? start_off : 0, count};
+  Segment seg;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    if (lane == 0 && count > 0) {
+      const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
+      int i = 0, segs = 0;
+      bool ok = true;
+      while (ok && walk.next(seg)) {
+        if (segs > 0) ok = mbar_wait_bounded(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128));
+        for (int c = 0; c < p.na; ++c)
+          tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, seg.b * a.Hq + h_base, q_full, keep);
+        ++segs;
+        for (int t = seg.t0; t < seg.t1; ++t, ++i) {
+          const int st = i % p.nstage, use = i / p.nstage;
+          const int tok = t * kTok;
+          const int page = __ldg(a.block_table + (size_t)seg.b * a.max_pages + tok / a.page_size);
+          // rows past the pool read as zeros: so do those of a page that is not mapped
+          const int row = page >= 0 && page < a.num_pages ? page * a.page_size + tok % a.page_size
+                                                          : a.num_pages * a.page_size;
+          if (use > 0 && !(ok = mbar_wait_bounded(&empty[st], (uint32_t)((use - 1) & 1), a.dev_status))) break;
+          mbar_arrive_expect_tx(&full[st], (uint32_t)(p.na * kAtom));
+          uint8_t* dst = smem + lay.stages + (uint32_t)st * p.sa * kAtom;
+          for (int c = 0; c < p.na; ++c)
+            tma_load_2d(dst + c * kAtom, &p.mc, 64 * c, row, &full[st], once);
+        }
+      }
+      // every requested copy lands before the shared memory is released (bounded; on the normal
+      // path nothing is outstanding: the MMA warp has waited for each)
+      if (segs > 0) mbar_wait_bounded(q_full, (uint32_t)((segs - 1) & 1), nullptr);
+      for (int k = max(0, i - p.nstage); k < i; ++k)
+        mbar_wait_bounded(&full[k % p.nstage], (uint32_t)((k / p.nstage) & 1), nullptr);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    const uint32_t id_s = idesc_bf16_f32(64, kTok, false, false);
+    const uint32_t id_o = idesc_bf16_f32(128, p.NH, true, false);
+    const uint32_t q_addr = smem_u32(smem), p_addr = smem_u32(smem + lay.p);
+    bool ok = true;
+    int i = 0, segs = 0;
+    auto stage_addr = [&](int k) { return smem_u32(smem + lay.stages) + (uint32_t)(k % p.nstage) * p.sa * kAtom; };
+    // the whole warp: wait for tile k (tile t of the segment), clear what lies past the length,
+    // and let lane 0 issue S
+    auto issue_s = [&](int k, int t) -> bool {
+      const bool got = mbar_wait_bounded(&full[k % p.nstage], (uint32_t)((k / p.nstage) & 1), a.dev_status);
+      if (!__all_sync(~0u, got)) return false;
+      const int valid = seg.L - t * kTok;
+      if (valid < kTok) {
+        uint8_t* tile = smem + lay.stages + (uint32_t)(k % p.nstage) * p.sa * kAtom;
+        const int nz = (a.r + 63) / 64, per_atom = (kTok - valid) * 8;
+        for (int e = lane; e < nz * per_atom; e += 32)
+          *reinterpret_cast<uint4*>(tile + (e / per_atom) * kAtom + valid * 128 + (e % per_atom) * 16) =
+              make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t d = tmem + kSCol + (uint32_t)(k & 1) * kTok, tile = stage_addr(k);
+        for (int c = 0; c < p.na; ++c) {
+          const int steps = min(4, (p.w - 64 * c) / 16);
+          for (int kk = 0; kk < steps; ++kk)
+            umma_bf16(d, sw128_desc(q_addr + (uint32_t)(c * p.NH * 128 + kk * 32)),
+                      sw128_desc(tile + (uint32_t)(c * kAtom + kk * 32)), id_s, c > 0 || kk > 0);
+        }
+        umma_commit(&s_full[k & 1]);
+        if (t == seg.t1 - 1) umma_commit(q_empty);  // the segment's last product with its q~
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && walk.next(seg)) {
+      ok = __all_sync(~0u, mbar_wait_bounded(q_full, (uint32_t)(segs & 1), a.dev_status));
+      ok = ok && issue_s(i, seg.t0);
+      for (int t = seg.t0; ok && t < seg.t1; ++t, ++i) {
+        if (t + 1 < seg.t1) {
+          if (!(ok = issue_s(i + 1, t + 1))) break;
+        }
+        if (t == seg.t0 && segs > 0 &&
+            !(ok = __all_sync(~0u, mbar_wait_bounded(o_free, (uint32_t)((segs - 1) & 1), a.dev_status))))
+          break;
+        if (!(ok = __all_sync(~0u, mbar_wait_bounded(p_full, (uint32_t)(i & 1), a.dev_status)))) break;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t tile = stage_addr(i);
+          for (int m = 0; m < p.nm; ++m)
+            for (int kk = 0; kk < kTok / 16; ++kk)
+              umma_bf16(tmem + (uint32_t)(m * p.NH), sw128_mn_desc(tile + (uint32_t)(2 * m * kAtom + kk * 2048), kAtom),
+                        sw128_desc(p_addr + (uint32_t)(kk * 32)), id_o, t > seg.t0 || kk > 0);
+          umma_commit(&empty[i % p.nstage]);
+          umma_commit(pv_done);
+        }
+        __syncwarp();
+      }
+      ++segs;
+    }
+    if (!ok && lane == 0) {  // products left by a timeout get a bounded chance to finish
+      umma_commit(drain);
+      mbar_wait_bounded(drain, 0u, nullptr);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax and output
+    const int quad = warp & 3, r0 = quad * 16 + (lane >> 2), col = 2 * (lane & 3);
+    const bool active = quad * 16 < p.NH;        // this warp's 16 heads exist (16 * quad + ...)
+    const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+    bool bad = false;  // a wait gave up
+    int i = 0;
+    while (walk.next(seg)) {
+      float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
+      for (int t = seg.t0; t < seg.t1; ++t, ++i) {
+        float x[32];
+        float f0 = 1.f, f1 = 1.f;
+        bool move = false;
+        if (active) {
+          bad |= !mbar_wait_bounded(&s_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status);
+          tc_fence_after();
+          uint32_t v[32];
+          tmem_ld_16x256b_x8(tmem + lane_addr + kSCol + (uint32_t)(i & 1) * kTok, v);
+          tmem_wait_ld();
+          const int valid = seg.L - t * kTok;
+          float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool in = 8 * j + col + e < valid;
+              x[4 * j + e] = in ? __uint_as_float(v[4 * j + e]) * p.scale2 : -INFINITY;
+              x[4 * j + 2 + e] = in ? __uint_as_float(v[4 * j + 2 + e]) * p.scale2 : -INFINITY;
+              t0 = fmaxf(t0, x[4 * j + e]);
+              t1 = fmaxf(t1, x[4 * j + 2 + e]);
+            }
+          t0 = fmaxf(t0, __shfl_xor_sync(~0u, t0, 1));
+          t1 = fmaxf(t1, __shfl_xor_sync(~0u, t1, 1));
+          t0 = fmaxf(t0, __shfl_xor_sync(~0u, t0, 2));
+          t1 = fmaxf(t1, __shfl_xor_sync(~0u, t1, 2));
+          if (t == seg.t0) {  // (a floor, so that a tile of -inf scores weighs 0 and not NaN)
+            m0 = fmaxf(t0, -1e30f);
+            m1 = fmaxf(t1, -1e30f);
+          } else {
+            if (t0 > m0 + kRescale) {
+              f0 = fast_exp2(m0 - t0);
+              m0 = t0;
+              move |= r0 < nheads;
+            }
+            if (t1 > m1 + kRescale) {
+              f1 = fast_exp2(m1 - t1);
+              m1 = t1;
+              move |= r0 + 8 < nheads;
+            }
+          }
+        }
+        if (named_bar_or(1, 128, move || bad)) {
+          if (named_bar_or(1, 128, bad)) break;
+          // some head's reference moved: scale its column of O~^T, once the last product is in
+          if (active && (lane & 3) == 0) {
+            sm_f[r0] = f0;
+            sm_f[r0 + 8] = f1;
+          }
+          bad |= !mbar_wait_bounded(pv_done, (uint32_t)((i - 1) & 1), a.dev_status);
+          if (named_bar_or(1, 128, bad)) break;
+          tc_fence_after();
+          for (int c = 0; c < p.nm * p.NH; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(tmem + lane_addr + (uint32_t)c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * sm_f[c % p.NH + e]);
+            tmem_st16(tmem + lane_addr + (uint32_t)c, v);
+          }
+          tmem_wait_st();
+        }
+        l0 *= f0;
+        l1 *= f1;
+        if (active) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            w[2 * j] = pack_bf16x2_rn(fast_exp2(x[4 * j] - m0), fast_exp2(x[4 * j + 1] - m0));
+            w[2 * j + 1] = pack_bf16x2_rn(fast_exp2(x[4 * j + 2] - m1), fast_exp2(x[4 * j + 3] - m1));
+            l0 += bf16lo(w[2 * j]) + bf16hi(w[2 * j]);
+            l1 += bf16lo(w[2 * j + 1]) + bf16hi(w[2 * j + 1]);
+          }
+          // P's buffer is free once the last tile's product is in
+          if (i > 0 && !mbar_wait_bounded(pv_done, (uint32_t)((i - 1) & 1), a.dev_status)) bad = true;
+          const uint32_t base = (uint32_t)r0 * 128u + (uint32_t)col * 2u;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t off = (uint32_t)((j ^ (r0 & 7)) << 4);
+            *reinterpret_cast<uint32_t*>(smem + lay.p + base + off) = w[2 * j];
+            *reinterpret_cast<uint32_t*>(smem + lay.p + base + 8 * 128 + off) = w[2 * j + 1];
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && !bad) mbar_arrive(p_full);
+      }
+      // the segment's sums; O~ is complete with its last tile's product
+      l0 += __shfl_xor_sync(~0u, l0, 1);
+      l1 += __shfl_xor_sync(~0u, l1, 1);
+      l0 += __shfl_xor_sync(~0u, l0, 2);
+      l1 += __shfl_xor_sync(~0u, l1, 2);
+      if (active && (lane & 3) == 0) {
+        sm_l[r0] = l0;
+        sm_l[r0 + 8] = l1;
+        sm_m[r0] = m0;
+        sm_m[r0 + 8] = m1;
+      }
+      if (!bad) bad = !mbar_wait_bounded(pv_done, (uint32_t)((i - 1) & 1), a.dev_status);
+      if (named_bar_or(1, 128, bad)) break;
+      tc_fence_after();
+      const int n = (seg.L + kTok - 1) / kTok;
+      const bool whole = seg.t0 == 0 && seg.t1 == n;
+      const int dim = quad * 32 + lane;
+      const int slot = ((int)blockIdx.x * 2 + (seg.first ? 0 : 1));
+      uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
+      float2* ml = reinterpret_cast<float2*>(ws + meta_bytes(a.B)) + (size_t)slot * kMaxHeads;
+      float* part = reinterpret_cast<float*>(ws + meta_bytes(a.B) + ml_bytes()) + (size_t)slot * p.NH * a.r;
+      for (int m = 0; m < p.nm; ++m)
+        for (int c = 0; c < p.NH; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c), v);
+          tmem_wait_ld();
+          const int d = m * 128 + dim;
+          if (d < a.r) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c + e < nheads) {
+                const float o = __uint_as_float(v[e]);
+                if (whole)
+                  a.out[((size_t)seg.b * a.Hq + h_base + c + e) * a.r + d] = f32_to_bf16_rn(o / sm_l[c + e]);
+                else
+                  part[(size_t)(c + e) * a.r + d] = o;
+              }
+          }
+        }
+      tc_fence_before();
+      const int th = tid - 128;
+      if (!whole && th < nheads) ml[th] = make_float2(sm_m[th], sm_l[th]);
+      // the CTAs that hold this sequence, for the merge: written by the one with its first tile
+      if (seg.t0 == 0 && th == 0 && group == 0) {
+        const long long first = g0 + i - (seg.t1 - seg.t0);
+        reinterpret_cast<int2*>(ws)[seg.b] =
+            make_int2(cta * 2 + (seg.first ? 0 : 1), whole ? -1 : (int)((first + n - 1) / per));
+      }
+      named_bar_sync(1, 128);  // sm_l, sm_m and O~ have been read
+      if (lane == 0) mbar_arrive(o_free);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
-size_t shared_decode_workspace_bytes(int B, int Hq, int r) { return (size_t)256 + 0 * ((size_t)B * Hq * r); }
+// Joins the partial states of sequences that several CTAs hold, and writes the zeros of empty
+// ones.  An item is 128 dims of one head: one warp (kWarps = 1), or a whole CTA whose warps
+// share the partial states (few sequences, many parts each).
+template <int kWarps>
+__global__ void __launch_bounds__(256) stief_shared_merge_kernel(const SharedDecodeArgs a, int NH, int groups, int G) {
+  __shared__ float4 acc_s[8][32];
+  __shared__ float red_s[8][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
+  const int nd = (a.r + 127) / 128;
+  const int item = kWarps == 1 ? (int)blockIdx.x * 8 + warp : (int)blockIdx.x;
+  const int h = item / nd, d = (item % nd) * 128 + lane * 4;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int L = valid_length(__ldg(a.seq_lens + b), a.max_seq_len);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
+  const int2 meta = L > 0 ? *reinterpret_cast<const int2*>(ws + (size_t)b * 8) : make_int2(0, 0);
+  if (L > 0 && meta.y < 0) return;  // whole: written already
+  if (h >= a.Hq) return;            // (kWarps == 8: never, the grid is exact)
+  uint16_t* out = a.out + ((size_t)b * a.Hq + h) * a.r + d;
+  if (L == 0) {
+    if (d < a.r && (kWarps == 1 || warp == 0)) *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
+    return;
+  }
+  // partial state k is in CTA c = meta.x / 2 + k of the head's group: slot 0 but for the first
+  const int group = h / NH, hl = h % NH, c_first = meta.x >> 1, n = meta.y - c_first + 1;
+  if (c_first < 0 || n < 1 || meta.y >= G) return;  // the first kernel gave up on a wait
+  const float2* ml = reinterpret_cast<const float2*>(ws + meta_bytes(a.B));
+  const float* part = reinterpret_cast<const float*>(ws + meta_bytes(a.B) + ml_bytes());
+  auto slot_of = [&](int k) { return ((c_first + k) * groups + group) * 2 + (k == 0 ? (meta.x & 1) : 0); };
+  float M = -INFINITY;
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, ml[(size_t)slot_of(k) * kMaxHeads + hl].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  const int w0 = kWarps == 1 ? 0 : warp;
+#pragma unroll 4
+  for (int k = w0; k < n; k += kWarps) {
+    const size_t s = (size_t)slot_of(k);
+    const float2 e = ml[s * kMaxHeads + hl];
+    const float4 o = d < a.r ? *reinterpret_cast<const float4*>(part + (s * NH + hl) * a.r + d)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float f = fast_exp2(e.x - M);
+    l += f * e.y;
+    acc.x += f * o.x;
+    acc.y += f * o.y;
+    acc.z += f * o.z;
+    acc.w += f * o.w;
+  }
+  if (kWarps > 1) {
+    acc_s[warp][lane] = acc;
+    if (lane == 0) red_s[warp][0] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    for (int k = 1; k < 8; ++k) {
+      const float4 o = acc_s[k][lane];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+      l += red_s[k][0];
+    }
+  }
+  if (d < a.r)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16x2_rn(acc.x / l, acc.y / l), pack_bf16x2_rn(acc.z / l, acc.w / l));
+}
+
+size_t shared_decode_workspace_bytes(int B, int Hq, int r) {
+  return meta_bytes(B) + ml_bytes() + (size_t)kMaxCtas * 2 * heads_per_cta(Hq) * r * 4;
+}
 
 cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream) {
-  stief_shared_decode_kernel<<<dim3(a.Hq, a.B), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  Args p{};
+  p.a = a;
+  p.w = a.r + a.dr;
+  p.na = (p.w + 63) / 64;
+  p.nm = (a.r + 127) / 128;
+  p.sa = p.na > 2 * p.nm ? p.na : 2 * p.nm;
+  p.NH = heads_per_cta(a.Hq);
+  p.groups = (a.Hq + p.NH - 1) / p.NH;
+  const int ctas = a.sms < kMaxCtas ? a.sms : kMaxCtas;
+  p.G = ctas / p.groups;
+  p.scale2 = a.scale * 1.4426950408889634f;
+  constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
+  for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage).total > kMost;)
+    --p.nstage;
+  uint32_t smem = layout_of(p.na, p.sa, p.NH, p.nstage).total;
+  if (smem > kMost) return cudaErrorInvalidValue;
+  if (smem < 120u * 1024u) smem = 120u * 1024u;  // one CTA an SM: it holds all of TMEM
+  if (!encode_tiled_bf16_2d(&p.mq, a.q, (uint64_t)p.w, (uint64_t)a.B * a.Hq, (uint64_t)p.w * 2, 64, (uint32_t)p.NH,
+                            CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_bf16_2d(&p.mc, a.pages, (uint64_t)p.w, (uint64_t)a.num_pages * a.page_size, (uint64_t)p.w * 2, 64,
+                            kTok, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  static SmemLimit limit;
+  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_shared_decode_kernel), a.device, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.G * p.groups);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, stief_shared_decode_kernel, p);
+  if (e != cudaSuccess) return e;
+  const int items = a.Hq * p.nm;
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  // many parts a sequence: a CTA an item, its warps share the parts; else a warp an item
+  if (p.G > 8 * a.B) {
+    cfg.gridDim = dim3(items, a.B);
+    return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<8>, a, p.NH, p.groups, p.G);
+  }
+  cfg.gridDim = dim3((items + 7) / 8, a.B);
+  return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<1>, a, p.NH, p.groups, p.G);
 }
 
 }  // namespace stief

@@ -606,7 +606,7 @@ STIEF_API stief_status stief_append_shared_paged(const uint16_t* c_new, const ui
  * over tokens [0, seq_lens[b]).  A sequence of length 0 gives zeros; a length that is negative
  * or above max_seq_len gives zeros and STIEF_DEV_BAD_LENGTH.  Rows at and past the length may
  * hold anything.  Pages that are not mapped read as zeros, as in the paged decode.
- * max_seq_len <= max_pages * page_size.  workspace: stief_decode_shared_workspace_bytes(B, Hq, r)
+ * max_seq_len <= max_pages * page_size, B * ceil(max_seq_len / 64) < 2^30.  workspace: stief_decode_shared_workspace_bytes(B, Hq, r)
  * bytes, 16-byte aligned; its contents do not matter before or after a call, but calls that may
  * overlap must not share it.
  * Products are bf16 on the tensor cores with fp32 sums; the weights enter the second product
