@@ -39,38 +39,38 @@ namespace stief {
 
 namespace {
 
-constexpr int kTok = 64;            // tokens per tile
-constexpr int kAtom = kTok * 128;   // bytes of one 64-column atom of a tile
+constexpr int kTile = 32;           // tokens per tile
 constexpr int kMaxHeads = 64;       // heads per CTA
 constexpr int kMaxStages = 8;
 constexpr int kThreads = 256;
 constexpr int kSoftWarps = 4;       // warps 4..7, one per TMEM lane quadrant
 constexpr int kMaxCtas = 160;       // the workspace holds two partial states for each
-constexpr int kMinTiles = 2;        // tiles per CTA at least (fewer would only add merging)
+constexpr int kMinTiles = 4;        // tiles per CTA at least (fewer would only add merging)
 constexpr uint32_t kSCol = 256;     // TMEM: O~^T at 0, S buffers at 256 and 320
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;     // log2 units the reference may lag behind
 
 struct Args {
   CUtensorMap mq;     // q [B * Hq][w], box 64 x heads
-  CUtensorMap mc;     // pool [rows][w], box 64 x 64
+  CUtensorMap mc;     // pool rows in blocks of 64 columns, box 64 x tile (x all blocks if w % 64 == 0)
   SharedDecodeArgs a;
   int w, na, sa, nm;  // row width, atoms loaded and atoms kept a tile, 128-dim tiles of o~
   int NH, groups, G;  // heads per CTA (a multiple of 16), head groups, CTAs per group
   int nstage;
+  int whole_rows;     // w % 64 == 0: one copy brings a tile's atoms
   float scale2;       // scale * log2(e)
 };
 
 struct Layout {
   uint32_t stages, p, ml, bars, total;
 };
-__host__ __device__ inline Layout layout_of(int na, int sa, int NH, int nstage) {
+__host__ __device__ inline Layout layout_of(int na, int sa, int NH, int nstage, int tile) {
   Layout l;
   l.stages = (uint32_t)na * NH * 128;  // q~ comes first
-  l.p = l.stages + (uint32_t)nstage * sa * kAtom;
+  l.p = l.stages + (uint32_t)nstage * sa * tile * 128;
   l.ml = l.p + (uint32_t)NH * 128;
   l.bars = l.ml + 3 * kMaxHeads * 4;
-  l.total = l.bars + 8 * (2 * kMaxStages + 8) + 64;
+  l.total = l.bars + 8 * (2 * kMaxStages + 9) + 56;
   return l;
 }
 
@@ -83,7 +83,23 @@ __host__ __device__ inline int heads_per_cta(int Hq) {
   return ((Hq + g - 1) / g + 15) / 16 * 16;
 }
 
+// Position in the ring of stages (counted up: a division by the stage count costs as much as
+// several products of the pipeline it would sit in).
+struct Ring {
+  int n, st = 0;
+  uint32_t ph = 0;  // parity of the stage's current use
+  __device__ __forceinline__ void next() {
+    if (++st == n) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
 __device__ __forceinline__ int valid_length(int L, int most) { return L < 0 || L > most ? 0 : L; }
+
+template <int kTok>
+__device__ __forceinline__ int tiles_of(int L) { return (L + kTok - 1) / kTok; }
 
 // The stretch of one sequence's tiles [t0, t1) that a CTA works on.
 struct Segment {
@@ -91,13 +107,14 @@ struct Segment {
   bool first;  // the CTA's first
 };
 // Walks the CTA's tiles sequence by sequence; every warp role walks the same way.
+template <int kTok>
 struct Walk {
   const int32_t* lens;
   int most, B, b, off, left;
   bool first = true;
   __device__ bool next(Segment& s) {
     while (left > 0 && b < B) {
-      const int L = valid_length(__ldg(lens + b), most), n = (L + kTok - 1) / kTok;
+      const int L = valid_length(__ldg(lens + b), most), n = tiles_of<kTok>(L);
       if (off >= n) {
         off = 0;
         ++b;
@@ -120,15 +137,17 @@ struct Walk {
 
 }  // namespace
 
+template <int kTok>
 __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const __grid_constant__ Args p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sum[8], start_b, start_off;
+  constexpr int kAtom = kTok * 128;  // bytes of one 64-column atom of a tile
   const SharedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = (int)blockIdx.x % p.groups, cta = (int)blockIdx.x / p.groups;
   const int h_base = group * p.NH, nheads = min(p.NH, a.Hq - h_base);
-  const Layout lay = layout_of(p.na, p.sa, p.NH, p.nstage);
+  const Layout lay = layout_of(p.na, p.sa, p.NH, p.nstage, kTok);
   float* sm_f = reinterpret_cast<float*>(smem + lay.ml);  // rescale factors
   float* sm_m = sm_f + kMaxHeads;
   float* sm_l = sm_m + kMaxHeads;
@@ -138,9 +157,9 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_full + 2;         // [2] S of a tile is in TMEM
   uint64_t* p_full = q_full + 4;         // P of a tile is in shared memory
-  uint64_t* pv_done = q_full + 5;        // O~ of a tile is added: P and O~ are free
-  uint64_t* o_free = q_full + 6;         // the segment's O~ has been read
-  uint64_t* drain = q_full + 7;
+  uint64_t* pv_done = q_full + 5;        // [2] O~ of a tile is added: its P and O~ are free
+  uint64_t* o_free = q_full + 7;         // the segment's O~ has been read
+  uint64_t* drain = q_full + 8;
 
   if ((smem_u32(smem) & 1023u) != 0) {  // swizzled operands need 1 KiB alignment
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
@@ -156,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(p_full, kSoftWarps);
-    mbar_init(pv_done, 1);
+    mbar_init(&pv_done[0], 1);
+    mbar_init(&pv_done[1], 1);
     mbar_init(o_free, kSoftWarps);
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -173,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   for (int b = c0; b < c1; ++b) {
     const int L = __ldg(a.seq_lens + b);
     if (valid_length(L, a.max_seq_len) != L && blockIdx.x == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
-    sum += (valid_length(L, a.max_seq_len) + kTok - 1) / kTok;
+    sum += tiles_of<kTok>(valid_length(L, a.max_seq_len));
   }
   int incl = sum;
 #pragma unroll
@@ -197,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   if (count > 0 && g0 >= incl - sum && g0 < incl) {  // one thread's sequences hold the first tile
     int at = incl - sum, b = c0;
     for (;; ++b) {
-      const int n = (valid_length(__ldg(a.seq_lens + b), a.max_seq_len) + kTok - 1) / kTok;
+      const int n = tiles_of<kTok>(valid_length(__ldg(a.seq_lens + b), a.max_seq_len));
       if (g0 < at + n) break;
       at += n;
     }
@@ -206,34 +226,50 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   }
   __syncthreads();
   const uint32_t tmem = tmem_slot;
-  Walk walk{a.seq_lens, a.max_seq_len, a.B, count > 0 ? start_b : 0, count > 0 ? start_off : 0, count};
+  Walk<kTok> walk{a.seq_lens, a.max_seq_len, a.B, count > 0 ? start_b : 0, count > 0 ? start_off : 0, count};
   Segment seg;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    if (lane == 0 && count > 0) {
+    if (count > 0) {
       const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
       int i = 0, segs = 0;
+      Ring ring{p.nstage};
       bool ok = true;
       while (ok && walk.next(seg)) {
-        if (segs > 0) ok = mbar_wait_bounded(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status);
+        if (segs > 0) ok = __all_sync(~0u, mbar_wait_bounded(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status));
         if (!ok) break;
-        mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128));
-        for (int c = 0; c < p.na; ++c)
-          tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, seg.b * a.Hq + h_base, q_full, keep);
-        ++segs;
-        for (int t = seg.t0; t < seg.t1; ++t, ++i) {
-          const int st = i % p.nstage, use = i / p.nstage;
-          const int tok = t * kTok;
-          const int page = __ldg(a.block_table + (size_t)seg.b * a.max_pages + tok / a.page_size);
-          // rows past the pool read as zeros: so do those of a page that is not mapped
-          const int row = page >= 0 && page < a.num_pages ? page * a.page_size + tok % a.page_size
-                                                          : a.num_pages * a.page_size;
-          if (use > 0 && !(ok = mbar_wait_bounded(&empty[st], (uint32_t)((use - 1) & 1), a.dev_status))) break;
-          mbar_arrive_expect_tx(&full[st], (uint32_t)(p.na * kAtom));
-          uint8_t* dst = smem + lay.stages + (uint32_t)st * p.sa * kAtom;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128));
           for (int c = 0; c < p.na; ++c)
-            tma_load_2d(dst + c * kAtom, &p.mc, 64 * c, row, &full[st], once);
+            tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, seg.b * a.Hq + h_base, q_full, keep);
+        }
+        __syncwarp();
+        ++segs;
+        const int32_t* entry = a.block_table + (size_t)seg.b * a.max_pages + seg.t0 * kTok / a.page_size;
+        int in_page = seg.t0 * kTok % a.page_size, page = __ldg(entry);
+        for (int t = seg.t0; t < seg.t1; ++t, ++i, ring.next()) {
+          if (in_page == a.page_size) {
+            in_page = 0;
+            page = __ldg(++entry);
+          }
+          // rows past the pool read as zeros: so do those of a page that is not mapped
+          const int row = page >= 0 && page < a.num_pages ? page * a.page_size + in_page
+                                                          : a.num_pages * a.page_size;
+          in_page += kTok;
+          const int st = ring.st;
+          if (i >= p.nstage && !(ok = __all_sync(~0u, mbar_wait_bounded(&empty[st], ring.ph ^ 1u, a.dev_status))))
+            break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&full[st], (uint32_t)(p.na * kAtom));
+            uint8_t* dst = smem + lay.stages + (uint32_t)(st * p.sa) * kAtom;
+            if (p.whole_rows) {
+              tma_load_3d(dst, &p.mc, 0, row, 0, &full[st], once);
+            } else {
+              for (int c = 0; c < p.na; ++c) tma_load_2d(dst + c * kAtom, &p.mc, 64 * c, row, &full[st], once);
+            }
+          }
+          __syncwarp();
         }
       }
       // every requested copy lands before the shared memory is released (bounded; on the normal
@@ -249,15 +285,16 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     const uint32_t q_addr = smem_u32(smem), p_addr = smem_u32(smem + lay.p);
     bool ok = true;
     int i = 0, segs = 0;
-    auto stage_addr = [&](int k) { return smem_u32(smem + lay.stages) + (uint32_t)(k % p.nstage) * p.sa * kAtom; };
+    Ring rs{p.nstage}, ro{p.nstage};  // the next tile to score, the next to add up
+    const uint32_t stage0 = smem_u32(smem + lay.stages), stage_bytes = (uint32_t)p.sa * kAtom;
     // the whole warp: wait for tile k (tile t of the segment), clear what lies past the length,
     // and let lane 0 issue S
     auto issue_s = [&](int k, int t) -> bool {
-      const bool got = mbar_wait_bounded(&full[k % p.nstage], (uint32_t)((k / p.nstage) & 1), a.dev_status);
+      const bool got = mbar_wait_bounded(&full[rs.st], rs.ph, a.dev_status);
       if (!__all_sync(~0u, got)) return false;
       const int valid = seg.L - t * kTok;
       if (valid < kTok) {
-        uint8_t* tile = smem + lay.stages + (uint32_t)(k % p.nstage) * p.sa * kAtom;
+        uint8_t* tile = smem + lay.stages + (uint32_t)rs.st * stage_bytes;
         const int nz = (a.r + 63) / 64, per_atom = (kTok - valid) * 8;
         for (int e = lane; e < nz * per_atom; e += 32)
           *reinterpret_cast<uint4*>(tile + (e / per_atom) * kAtom + valid * 128 + (e % per_atom) * 16) =
@@ -265,43 +302,60 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after();
-        const uint32_t d = tmem + kSCol + (uint32_t)(k & 1) * kTok, tile = stage_addr(k);
-        for (int c = 0; c < p.na; ++c) {
-          const int steps = min(4, (p.w - 64 * c) / 16);
-          for (int kk = 0; kk < steps; ++kk)
-            umma_bf16(d, sw128_desc(q_addr + (uint32_t)(c * p.NH * 128 + kk * 32)),
-                      sw128_desc(tile + (uint32_t)(c * kAtom + kk * 32)), id_s, c > 0 || kk > 0);
+        // (descriptors advance by additions, four steps at a time: building each one took longer
+        // than its product)
+        const uint32_t d = tmem + kSCol + (uint32_t)(k & 1) * kTok;
+        uint64_t dq = sw128_desc(q_addr), dt = sw128_desc(stage0 + (uint32_t)rs.st * stage_bytes);
+        int left = p.w / 16;
+        for (; left >= 4; left -= 4) {
+          umma_bf16(d, dq, dt, id_s, left != p.w / 16);
+          umma_bf16(d, dq + 2, dt + 2, id_s, 1);
+          umma_bf16(d, dq + 4, dt + 4, id_s, 1);
+          umma_bf16(d, dq + 6, dt + 6, id_s, 1);
+          dq += (uint64_t)(p.NH * 128) >> 4;
+          dt += kAtom >> 4;
         }
+        for (int kk = 0; kk < left; ++kk) umma_bf16(d, dq + 2 * kk, dt + 2 * kk, id_s, kk > 0 || p.w >= 64);
         umma_commit(&s_full[k & 1]);
         if (t == seg.t1 - 1) umma_commit(q_empty);  // the segment's last product with its q~
       }
       __syncwarp();
+      rs.next();
       return true;
     };
     while (ok && walk.next(seg)) {
       ok = __all_sync(~0u, mbar_wait_bounded(q_full, (uint32_t)(segs & 1), a.dev_status));
       ok = ok && issue_s(i, seg.t0);
+      bool ahead = false;  // S of tile i is issued
       for (int t = seg.t0; ok && t < seg.t1; ++t, ++i) {
-        if (t + 1 < seg.t1) {
-          if (!(ok = issue_s(i + 1, t + 1))) break;
-        }
+        if (t > seg.t0 && !ahead && !(ok = issue_s(i, t))) break;
+        // the next tile's S goes first if its rows are in; otherwise this tile's product does
+        ahead = t + 1 < seg.t1 && __shfl_sync(~0u, mbar_test(&full[rs.st], rs.ph), 0);
+        if (ahead && !(ok = issue_s(i + 1, t + 1))) break;
         if (t == seg.t0 && segs > 0 &&
             !(ok = __all_sync(~0u, mbar_wait_bounded(o_free, (uint32_t)((segs - 1) & 1), a.dev_status))))
           break;
         if (!(ok = __all_sync(~0u, mbar_wait_bounded(p_full, (uint32_t)(i & 1), a.dev_status)))) break;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_fence_after();
-          const uint32_t tile = stage_addr(i);
-          for (int m = 0; m < p.nm; ++m)
-            for (int kk = 0; kk < kTok / 16; ++kk)
-              umma_bf16(tmem + (uint32_t)(m * p.NH), sw128_mn_desc(tile + (uint32_t)(2 * m * kAtom + kk * 2048), kAtom),
-                        sw128_desc(p_addr + (uint32_t)(kk * 32)), id_o, t > seg.t0 || kk > 0);
-          umma_commit(&empty[i % p.nstage]);
-          umma_commit(pv_done);
+          uint64_t dt = sw128_mn_desc(stage0 + (uint32_t)ro.st * stage_bytes, kAtom);
+          const uint64_t dp = sw128_desc(p_addr + (kTok == 32 ? (uint32_t)(i & 1) * 64u : 0u));
+          for (int m = 0; m < p.nm; ++m, dt += 2 * kAtom >> 4) {
+            const uint32_t d = tmem + (uint32_t)(m * p.NH);
+            umma_bf16(d, dt, dp, id_o, t > seg.t0);
+            umma_bf16(d, dt + 128, dp + 2, id_o, 1);
+            if (kTok == 64) {
+              umma_bf16(d, dt + 256, dp + 4, id_o, 1);
+              umma_bf16(d, dt + 384, dp + 6, id_o, 1);
+            }
+          }
+          umma_commit(&empty[ro.st]);
+          umma_commit(&pv_done[i & 1]);
         }
         __syncwarp();
+        ro.next();
       }
       ++segs;
     }
@@ -319,19 +373,19 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     while (walk.next(seg)) {
       float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
       for (int t = seg.t0; t < seg.t1; ++t, ++i) {
-        float x[32];
+        float x[kTok / 2];
         float f0 = 1.f, f1 = 1.f;
         bool move = false;
         if (active) {
           bad |= !mbar_wait_bounded(&s_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status);
           tc_fence_after();
-          uint32_t v[32];
-          tmem_ld_16x256b_x8(tmem + lane_addr + kSCol + (uint32_t)(i & 1) * kTok, v);
+          uint32_t v[kTok / 2];
+          tmem_ld_16x256b(tmem + lane_addr + kSCol + (uint32_t)(i & 1) * kTok, v);
           tmem_wait_ld();
           const int valid = seg.L - t * kTok;
           float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < kTok / 8; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const bool in = 8 * j + col + e < valid;
@@ -367,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
             sm_f[r0] = f0;
             sm_f[r0 + 8] = f1;
           }
-          bad |= !mbar_wait_bounded(pv_done, (uint32_t)((i - 1) & 1), a.dev_status);
+          bad |= !mbar_wait_bounded(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
           if (named_bar_or(1, 128, bad)) break;
           tc_fence_after();
           for (int c = 0; c < p.nm * p.NH; c += 16) {
@@ -383,20 +437,25 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
         l0 *= f0;
         l1 *= f1;
         if (active) {
-          uint32_t w[16];
+          uint32_t w[kTok / 4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < kTok / 8; ++j) {
             w[2 * j] = pack_bf16x2_rn(fast_exp2(x[4 * j] - m0), fast_exp2(x[4 * j + 1] - m0));
             w[2 * j + 1] = pack_bf16x2_rn(fast_exp2(x[4 * j + 2] - m1), fast_exp2(x[4 * j + 3] - m1));
             l0 += bf16lo(w[2 * j]) + bf16hi(w[2 * j]);
             l1 += bf16lo(w[2 * j + 1]) + bf16hi(w[2 * j + 1]);
           }
-          // P's buffer is free once the last tile's product is in
-          if (i > 0 && !mbar_wait_bounded(pv_done, (uint32_t)((i - 1) & 1), a.dev_status)) bad = true;
+          // P's buffer is free once the product of the last tile that used it is in: rows of 128
+          // bytes hold one tile of 64 tokens, or two of 32 in turn
+          constexpr int kBack = 64 / kTok;
+          if (i >= kBack &&
+              !mbar_wait_bounded(&pv_done[(i - kBack) & 1], (uint32_t)(((i - kBack) >> 1) & 1), a.dev_status))
+            bad = true;
           const uint32_t base = (uint32_t)r0 * 128u + (uint32_t)col * 2u;
+          const int j0 = kTok == 32 ? (i & 1) * 4 : 0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t off = (uint32_t)((j ^ (r0 & 7)) << 4);
+          for (int j = 0; j < kTok / 8; ++j) {
+            const uint32_t off = (uint32_t)(((j0 + j) ^ (r0 & 7)) << 4);
             *reinterpret_cast<uint32_t*>(smem + lay.p + base + off) = w[2 * j];
             *reinterpret_cast<uint32_t*>(smem + lay.p + base + 8 * 128 + off) = w[2 * j + 1];
           }
@@ -414,37 +473,41 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       if (active && (lane & 3) == 0) {
         sm_l[r0] = l0;
         sm_l[r0 + 8] = l1;
+        sm_f[r0] = 1.f / l0;
+        sm_f[r0 + 8] = 1.f / l1;
         sm_m[r0] = m0;
         sm_m[r0 + 8] = m1;
       }
-      if (!bad) bad = !mbar_wait_bounded(pv_done, (uint32_t)((i - 1) & 1), a.dev_status);
+      if (!bad) bad = !mbar_wait_bounded(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
       if (named_bar_or(1, 128, bad)) break;
       tc_fence_after();
-      const int n = (seg.L + kTok - 1) / kTok;
+      const int n = tiles_of<kTok>(seg.L);
       const bool whole = seg.t0 == 0 && seg.t1 == n;
       const int dim = quad * 32 + lane;
       const int slot = ((int)blockIdx.x * 2 + (seg.first ? 0 : 1));
       uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
       float2* ml = reinterpret_cast<float2*>(ws + meta_bytes(a.B)) + (size_t)slot * kMaxHeads;
       float* part = reinterpret_cast<float*>(ws + meta_bytes(a.B) + ml_bytes()) + (size_t)slot * p.NH * a.r;
-      for (int m = 0; m < p.nm; ++m)
+      for (int m = 0; m < p.nm; ++m) {
+        const int d = m * 128 + dim;
         for (int c = 0; c < p.NH; c += 16) {
           uint32_t v[16];
           tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c), v);
           tmem_wait_ld();
-          const int d = m * 128 + dim;
-          if (d < a.r) {
+          const int nh = d < a.r ? min(16, nheads - c) : 0;  // heads to store
+          if (whole) {
+            uint16_t* o = a.out + ((size_t)seg.b * a.Hq + h_base + c) * a.r + d;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (c + e < nheads) {
-                const float o = __uint_as_float(v[e]);
-                if (whole)
-                  a.out[((size_t)seg.b * a.Hq + h_base + c + e) * a.r + d] = f32_to_bf16_rn(o / sm_l[c + e]);
-                else
-                  part[(size_t)(c + e) * a.r + d] = o;
-              }
+              if (e < nh) o[(size_t)e * a.r] = f32_to_bf16_rn(__uint_as_float(v[e]) * sm_f[c + e]);
+          } else {
+            float* o = part + (size_t)c * a.r + d;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e < nh) o[(size_t)e * a.r] = __uint_as_float(v[e]);
           }
         }
+      }
       tc_fence_before();
       const int th = tid - 128;
       if (!whole && th < nheads) ml[th] = make_float2(sm_m[th], sm_l[th]);
@@ -552,18 +615,25 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   p.G = ctas / p.groups;
   p.scale2 = a.scale * 1.4426950408889634f;
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
-  for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage).total > kMost;)
+  const int tile = kTile;
+  for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage, tile).total > kMost;)
     --p.nstage;
-  uint32_t smem = layout_of(p.na, p.sa, p.NH, p.nstage).total;
+  uint32_t smem = layout_of(p.na, p.sa, p.NH, p.nstage, tile).total;
   if (smem > kMost) return cudaErrorInvalidValue;
   if (smem < 120u * 1024u) smem = 120u * 1024u;  // one CTA an SM: it holds all of TMEM
-  if (!encode_tiled_bf16_2d(&p.mq, a.q, (uint64_t)p.w, (uint64_t)a.B * a.Hq, (uint64_t)p.w * 2, 64, (uint32_t)p.NH,
-                            CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tiled_bf16_2d(&p.mc, a.pages, (uint64_t)p.w, (uint64_t)a.num_pages * a.page_size, (uint64_t)p.w * 2, 64,
-                            kTok, CU_TENSOR_MAP_SWIZZLE_128B))
+  const uint64_t rows = (uint64_t)a.num_pages * a.page_size, pitch = (uint64_t)p.w * 2;
+  p.whole_rows = p.w % 64 == 0;
+  if (!encode_tiled_bf16_2d(&p.mq, a.q, (uint64_t)p.w, (uint64_t)a.B * a.Hq, pitch, 64, (uint32_t)p.NH,
+                            CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  if (!(p.whole_rows ? encode_tiled_bf16_3d(&p.mc, a.pages, {64, rows, (uint64_t)p.na}, {pitch, 128},
+                                            {64, (uint32_t)tile, (uint32_t)p.na})
+                     : encode_tiled_bf16_2d(&p.mc, a.pages, (uint64_t)p.w, rows, pitch, 64, (uint32_t)tile,
+                                            CU_TENSOR_MAP_SWIZZLE_128B)))
+    return cudaErrorInvalidValue;
+  const auto kern = stief_shared_decode_kernel<kTile>;
   static SmemLimit limit;
-  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_shared_decode_kernel), a.device, (int)smem);
+  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kern), a.device, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -575,7 +645,7 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, stief_shared_decode_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return e;
   const int items = a.Hq * p.nm;
   cfg.blockDim = dim3(256);

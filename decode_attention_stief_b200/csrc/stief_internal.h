@@ -148,6 +148,11 @@ bool encode_tiled_bf16_2d(CUtensorMap* map, const void* base, uint64_t cols, uin
                           uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
                           CUtensorMapSwizzle swizzle);
 
+// 3-D tiled TMA tensor map over bf16 elements: dims (innermost first), byte strides of dims 1 and
+// 2, boxes, 128-byte swizzle (box[0] = 64 columns).  Host only.
+bool encode_tiled_bf16_3d(CUtensorMap* map, const void* base, const uint64_t (&dims)[3],
+                          const uint64_t (&strides)[2], const uint32_t (&box)[3]);
+
 struct CompressTcArgs;
 uint32_t compress_tc_smem_bytes(int rK, int rV);
 
