@@ -17,8 +17,8 @@
 // and r = 512 it takes 256 TMEM columns, half of the SM's, and the heads are the MMA's N, so
 // few heads cost few cycles.  More than 64 heads are split over CTAs that run side by side and
 // read the tiles through L2.
-//   warp 0: TMA producer; warp 1: MMA issuer (it also zeroes the rows past the length in a
-//   sequence's last tile: they may hold NaN, and 0 * NaN is NaN); warps 4-7: softmax, rescaling
+//   warp 0: TMA producer; warp 1: MMA issuer; warp 2: zeroes the rows past the length in a
+//   sequence's last tile (they may hold NaN, and 0 * NaN is NaN); warps 4-7: softmax, rescaling
 //   and the output.  S(i + 1) is issued before O(i), so the tensor cores work during softmax(i).
 // The running maximum is a reference that only moves when a score passes it by more than 2^8:
 // the accumulator is then rescaled in TMEM (rare); weights are at most 2^8 and rounded to bf16
@@ -39,13 +39,13 @@ namespace stief {
 
 namespace {
 
-constexpr int kTile = 32;           // tokens per tile
+constexpr int kTile = 64;           // tokens per tile
 constexpr int kMaxHeads = 64;       // heads per CTA
 constexpr int kMaxStages = 8;
 constexpr int kThreads = 256;
 constexpr int kSoftWarps = 4;       // warps 4..7, one per TMEM lane quadrant
 constexpr int kMaxCtas = 160;       // the workspace holds two partial states for each
-constexpr int kMinTiles = 4;        // tiles per CTA at least (fewer would only add merging)
+constexpr int kMinTiles = 2;        // tiles per CTA at least (fewer would only add merging)
 constexpr uint32_t kSCol = 256;     // TMEM: O~^T at 0, S buffers at 256 and 320
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;     // log2 units the reference may lag behind
@@ -70,7 +70,7 @@ __host__ __device__ inline Layout layout_of(int na, int sa, int NH, int nstage, 
   l.p = l.stages + (uint32_t)nstage * sa * tile * 128;
   l.ml = l.p + (uint32_t)NH * 128;
   l.bars = l.ml + 3 * kMaxHeads * 4;
-  l.total = l.bars + 8 * (2 * kMaxStages + 9) + 56;
+  l.total = l.bars + 8 * (2 * kMaxStages + 12) + 32;
   return l;
 }
 
@@ -160,6 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   uint64_t* pv_done = q_full + 5;        // [2] O~ of a tile is added: its P and O~ are free
   uint64_t* o_free = q_full + 7;         // the segment's O~ has been read
   uint64_t* drain = q_full + 8;
+  uint64_t* partial = q_full + 9;        // a sequence's last tile is in and is not full
+  uint64_t* tail = q_full + 10;          // its rows past the length are cleared
+  volatile uint32_t* stop = reinterpret_cast<uint32_t*>(q_full + 11);  // the issuer gave up
 
   if ((smem_u32(smem) & 1023u) != 0) {  // swizzled operands need 1 KiB alignment
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
@@ -179,6 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     mbar_init(&pv_done[1], 1);
     mbar_init(o_free, kSoftWarps);
     mbar_init(drain, 1);
+    mbar_init(partial, 1);
+    mbar_init(tail, 1);
+    *stop = 0;
     fence_barrier_init();
     prefetch_tensormap(&p.mq);
     prefetch_tensormap(&p.mc);
@@ -287,58 +293,56 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     int i = 0, segs = 0;
     Ring rs{p.nstage}, ro{p.nstage};  // the next tile to score, the next to add up
     const uint32_t stage0 = smem_u32(smem + lay.stages), stage_bytes = (uint32_t)p.sa * kAtom;
-    // the whole warp: wait for tile k (tile t of the segment), clear what lies past the length,
-    // and let lane 0 issue S
-    auto issue_s = [&](int k, int t) -> bool {
-      const bool got = mbar_wait_bounded(&full[rs.st], rs.ph, a.dev_status);
-      if (!__all_sync(~0u, got)) return false;
-      const int valid = seg.L - t * kTok;
-      if (valid < kTok) {
-        uint8_t* tile = smem + lay.stages + (uint32_t)rs.st * stage_bytes;
-        const int nz = (a.r + 63) / 64, per_atom = (kTok - valid) * 8;
-        for (int e = lane; e < nz * per_atom; e += 32)
-          *reinterpret_cast<uint4*>(tile + (e / per_atom) * kAtom + valid * 128 + (e % per_atom) * 16) =
-              make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (elect_one()) {
+    const uint32_t q_step = (uint32_t)(p.NH * 128) >> 4;
+    const int steps_left = p.w % 64 / 16;
+    // One thread runs the whole loop: under the products' shared-memory traffic every barrier
+    // test, shuffle or vote between them costs 100 cycles and more.
+    if (elect_one()) {
+      int tails = 0;
+      // S of tile k (tile t of the segment) once its rows are in
+      auto issue_s = [&](int k, int t, bool landed) -> bool {
+        if (!landed && !mbar_wait_bounded(&full[rs.st], rs.ph, a.dev_status)) return false;
+        if ((t + 1) * kTok > seg.L) {  // what lies past the length has been cleared
+          mbar_arrive(partial);
+          if (!mbar_wait_bounded(tail, (uint32_t)(tails & 1), a.dev_status)) return false;
+          ++tails;
+        }
         tc_fence_after();
         // (descriptors advance by additions, four steps at a time: building each one took longer
         // than its product)
         const uint32_t d = tmem + kSCol + (uint32_t)(k & 1) * kTok;
         uint64_t dq = sw128_desc(q_addr), dt = sw128_desc(stage0 + (uint32_t)rs.st * stage_bytes);
-        int left = p.w / 16;
-        for (; left >= 4; left -= 4) {
-          umma_bf16(d, dq, dt, id_s, left != p.w / 16);
+        uint32_t acc = 0;
+        for (int c = 0; c < p.w / 64; ++c) {
+          umma_bf16(d, dq, dt, id_s, acc);
           umma_bf16(d, dq + 2, dt + 2, id_s, 1);
           umma_bf16(d, dq + 4, dt + 4, id_s, 1);
           umma_bf16(d, dq + 6, dt + 6, id_s, 1);
-          dq += (uint64_t)(p.NH * 128) >> 4;
+          dq += q_step;
           dt += kAtom >> 4;
+          acc = 1;
         }
-        for (int kk = 0; kk < left; ++kk) umma_bf16(d, dq + 2 * kk, dt + 2 * kk, id_s, kk > 0 || p.w >= 64);
+        for (int kk = 0; kk < steps_left; ++kk) {
+          umma_bf16(d, dq + 2 * kk, dt + 2 * kk, id_s, acc);
+          acc = 1;
+        }
         umma_commit(&s_full[k & 1]);
         if (t == seg.t1 - 1) umma_commit(q_empty);  // the segment's last product with its q~
-      }
-      __syncwarp();
-      rs.next();
-      return true;
-    };
-    while (ok && walk.next(seg)) {
-      ok = __all_sync(~0u, mbar_wait_bounded(q_full, (uint32_t)(segs & 1), a.dev_status));
-      ok = ok && issue_s(i, seg.t0);
-      bool ahead = false;  // S of tile i is issued
-      for (int t = seg.t0; ok && t < seg.t1; ++t, ++i) {
-        if (t > seg.t0 && !ahead && !(ok = issue_s(i, t))) break;
-        // the next tile's S goes first if its rows are in; otherwise this tile's product does
-        ahead = t + 1 < seg.t1 && __shfl_sync(~0u, mbar_test(&full[rs.st], rs.ph), 0);
-        if (ahead && !(ok = issue_s(i + 1, t + 1))) break;
-        if (t == seg.t0 && segs > 0 &&
-            !(ok = __all_sync(~0u, mbar_wait_bounded(o_free, (uint32_t)((segs - 1) & 1), a.dev_status))))
-          break;
-        if (!(ok = __all_sync(~0u, mbar_wait_bounded(p_full, (uint32_t)(i & 1), a.dev_status)))) break;
-        if (elect_one()) {
+        rs.next();
+        return true;
+      };
+      while (ok && walk.next(seg)) {
+        ok = mbar_wait_bounded(q_full, (uint32_t)(segs & 1), a.dev_status) && issue_s(i, seg.t0, false);
+        bool ahead = true;  // S of tile i is issued
+        for (int t = seg.t0; ok && t < seg.t1; ++t, ++i) {
+          if (!ahead && !(ok = issue_s(i, t, false))) break;
+          // the next tile's S goes first if its rows are in; otherwise this tile's product does
+          ahead = t + 1 < seg.t1 && mbar_test(&full[rs.st], rs.ph);
+          if (ahead && !(ok = issue_s(i + 1, t + 1, true))) break;
+          if (t == seg.t0 && segs > 0 &&
+              !(ok = mbar_wait_bounded(o_free, (uint32_t)((segs - 1) & 1), a.dev_status)))
+            break;
+          if (!(ok = mbar_wait_bounded(p_full, (uint32_t)(i & 1), a.dev_status))) break;
           tc_fence_after();
           uint64_t dt = sw128_mn_desc(stage0 + (uint32_t)ro.st * stage_bytes, kAtom);
           const uint64_t dp = sw128_desc(p_addr + (kTok == 32 ? (uint32_t)(i & 1) * 64u : 0u));
@@ -353,15 +357,40 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
           }
           umma_commit(&empty[ro.st]);
           umma_commit(&pv_done[i & 1]);
+          ro.next();
         }
-        __syncwarp();
-        ro.next();
+        ++segs;
       }
-      ++segs;
+      if (!ok) {
+        *stop = 1;
+        // products left by a timeout get a bounded chance to finish
+        umma_commit(drain);
+        mbar_wait_bounded(drain, 0u, nullptr);
+      }
     }
-    if (!ok && lane == 0) {  // products left by a timeout get a bounded chance to finish
-      umma_commit(drain);
-      mbar_wait_bounded(drain, 0u, nullptr);
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- rows past the length
+    int i = 0, tails = 0;
+    while (walk.next(seg)) {
+      i += seg.t1 - seg.t0;
+      const int valid = seg.L - (seg.t1 - 1) * kTok;
+      if (valid >= kTok) continue;
+      const int k = i - 1, st = k % p.nstage;
+      // The issuer says when the tile is in (waiting on the stage itself could see an earlier
+      // use), or that it gave up; the wait spans the whole segment, hence the wider limit.
+      const uint64_t since = global_timer_ns();
+      bool got = mbar_try_wait(partial, (uint32_t)(tails & 1));
+      while (!got && *stop == 0 && global_timer_ns() - since < 32 * kWaitLimitNs)
+        got = mbar_try_wait(partial, (uint32_t)(tails & 1));
+      if (!__all_sync(~0u, got)) break;
+      ++tails;
+      uint8_t* tile = smem + lay.stages + (uint32_t)(st * p.sa) * kAtom;
+      for (int c = 0; c < (a.r + 63) / 64; ++c)
+        for (int e = valid * 8 + lane; e < kTok * 8; e += 32)
+          *reinterpret_cast<uint4*>(tile + c * kAtom + e * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tail);
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax and output
@@ -488,23 +517,26 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
       float2* ml = reinterpret_cast<float2*>(ws + meta_bytes(a.B)) + (size_t)slot * kMaxHeads;
       float* part = reinterpret_cast<float*>(ws + meta_bytes(a.B) + ml_bytes()) + (size_t)slot * p.NH * a.r;
+      // 32 heads' columns at a time: one wait for two loads, then a run of stores (a warp's 32
+      // neighbouring dims of one head each)
       for (int m = 0; m < p.nm; ++m) {
         const int d = m * 128 + dim;
-        for (int c = 0; c < p.NH; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c), v);
+        for (int c = 0; c < p.NH; c += 32) {
+          uint32_t v[2][16];
+          tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c), v[0]);
+          if (c + 16 < p.NH) tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c + 16), v[1]);
           tmem_wait_ld();
-          const int nh = d < a.r ? min(16, nheads - c) : 0;  // heads to store
+          const int nh = d < a.r ? nheads - c : 0;  // heads to store
           if (whole) {
             uint16_t* o = a.out + ((size_t)seg.b * a.Hq + h_base + c) * a.r + d;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (e < nh) o[(size_t)e * a.r] = f32_to_bf16_rn(__uint_as_float(v[e]) * sm_f[c + e]);
+            for (int e = 0; e < 32; ++e, o += a.r)
+              if (e < nh) *o = f32_to_bf16_rn(__uint_as_float(v[e >> 4][e & 15]) * sm_f[c + e]);
           } else {
             float* o = part + (size_t)c * a.r + d;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (e < nh) o[(size_t)e * a.r] = __uint_as_float(v[e]);
+            for (int e = 0; e < 32; ++e, o += a.r)
+              if (e < nh) *o = __uint_as_float(v[e >> 4][e & 15]);
           }
         }
       }
