@@ -1,47 +1,463 @@
 // prefill_attention.cu -- causal attention of ragged prompts over per-head keys and values, for
 // sm_100a.  Query i of sequence b (n_q queries, n_k keys) sees keys j <= i + n_k - n_q:
-//     o_i = softmax_j(scale * (q_i . k_j + q^R_i . k^R_j)) v_j.
-// This kernel: one warp a query row, an online softmax in fp32.
+//     o_i = softmax_j(scale * (q_i . k_j + q^R_i . k^R_j)) v_j,
+// one pass over the keys with a running maximum and sum.
+//
+// What bounds it: the products (2 (256 + dr) operations a visible pair and head) and, nearly as
+// long, one exponential a pair: 16 a cycle on an SM against 4096 multiply-adds.
+//
+// A CTA takes 256 queries of one head as two tiles of 128 and walks the keys in tiles of 128;
+// both products run on tcgen05 with M = N = 128:
+//     S_w = Q_w . K^T      (Q, K in shared memory, K-major, 128-byte swizzle)
+//     O_w += P_w . V       (P in tensor memory, V MN-major as it lies in memory)
+// TMEM holds S_0, S_1, O_0, O_1, 128 columns each: all of it.  P_w overwrites S_w, whose row a
+// thread holds in registers meanwhile.  The issuer alternates O_0, S_0', O_1, S_1', so that the
+// tensor cores work for one tile of queries while the softmax of the other runs.
+//   warp 0: TMA producer; warp 1: MMA issuer; warp 2: zeroes the value rows past n_k in the last
+//   tile (they may hold NaN, and 0 * NaN is NaN); warps 4-7 and 8-11: softmax of the two tiles,
+//   one thread a query row, and the output.
+// The reference of the running maximum moves only when a score passes it by more than 2^8 (as in
+// the decode): a warp then rescales its own rows of O_w, whose last product is complete when S_w
+// of the next tile is, because the products run in order.
+// CTAs start with the longest tiles of queries; a tile of queries none of whose rows exists ends
+// at once.
 #include <cstdint>
 
 #include "shared_latent.h"
 #include "stief_device.cuh"
+#include "umma.cuh"
 
 namespace stief {
 
-__global__ void __launch_bounds__(128) stief_prefill_kernel(const PrefillArgs a) {
-  const int lane = threadIdx.x & 31, i = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
-  const int q0 = a.q_start[b], nq = a.q_start[b + 1] - q0, k0 = a.kv_start[b], nk = a.kv_start[b + 1] - k0;
-  if (q0 < 0 || nq < 0 || k0 < 0 || nk < 0 || q0 + nq > a.Nq || k0 + nk > a.Nkv || nq > a.max_q) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
+namespace {
+
+constexpr int kRows = 128;                 // queries a tile, keys a tile
+constexpr uint32_t kAtom = kRows * 128;    // bytes of 128 rows x 64 columns
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 256;            // S_w at 128 w, O_w at 256 + 128 w
+constexpr float kRescale = 8.f;
+constexpr float kFloor = -1e30f;
+constexpr int kMaxSlots = 3;
+
+struct Args {
+  CUtensorMap mq;   // q [Nq][Hq * (128 + dr)], box 64 x 128
+  CUtensorMap mk;   // k [Nkv][Hkv * 128], box 64 x 128
+  CUtensorMap mv;   // v, same
+  CUtensorMap mp;   // k_pe [Nkv][dr], box 64 x 128
+  PrefillArgs a;
+  int atoms;        // 64-column atoms of a query or key row: 2, or 3 with a position part
+  int nk, nv;       // key and value slots
+  int qtiles;       // tiles of 256 queries of the longest sequence
+  float scale2;     // |scale| * log2(e)
+  int negate;       // scale < 0: the products are negated instead
+};
+
+struct Layout {
+  uint32_t k, v, bars, total;
+};
+__host__ __device__ inline Layout layout_of(int atoms, int nk, int nv) {
+  Layout l;
+  l.k = 2u * atoms * kAtom;
+  l.v = l.k + (uint32_t)nk * atoms * kAtom;
+  l.bars = l.v + (uint32_t)nv * 2 * kAtom;
+  l.total = l.bars + 8 * (4 * kMaxSlots + 16);
+  return l;
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid_constant__ Args p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint32_t tmem_slot;
+  const PrefillArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Layout lay = layout_of(p.atoms, p.nk, p.nv);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + lay.bars);
+  uint64_t* k_empty = k_full + kMaxSlots;
+  uint64_t* v_full = k_empty + kMaxSlots;
+  uint64_t* v_empty = v_full + kMaxSlots;
+  uint64_t* q_full = v_empty + kMaxSlots;  // [2]
+  uint64_t* s_full = q_full + 2;           // [2] S_w of a tile is in TMEM (and O_w before it)
+  uint64_t* p_full = q_full + 4;           // [2] P_w is in TMEM
+  uint64_t* o_full = q_full + 6;           // [2] O_w is complete
+  uint64_t* partial = q_full + 8;          // the last value tile is in and is not full
+  uint64_t* tail = q_full + 9;             // its rows past n_k are cleared
+  uint64_t* drain = q_full + 10;
+
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
     return;
   }
-  if (i >= nq) return;
-  const int dq = 128 + a.dr, hk = h / (a.Hq / a.Hkv);
-  const uint16_t* q = a.q + ((size_t)(q0 + i) * a.Hq + h) * dq;
-  float x[6], o[4] = {}, m = -INFINITY, l = 0.f;
-  for (int c = 0; c < 6; ++c) x[c] = lane + 32 * c < dq ? bf16_to_f32(q[lane + 32 * c]) * a.scale : 0.f;
-  const int seen = min(nk, i + nk - nq + 1);
-  for (int j = 0; j < seen; ++j) {
-    const uint16_t* k = a.k + ((size_t)(k0 + j) * a.Hkv + hk) * 128;
-    const uint16_t* v = a.v + ((size_t)(k0 + j) * a.Hkv + hk) * 128;
-    float s = 0.f;
-    for (int c = 0; c < 4; ++c) s += x[c] * bf16_to_f32(k[lane + 32 * c]);
-    for (int c = 4; c < 6; ++c)
-      if (lane + 32 * c < dq) s += x[c] * bf16_to_f32(a.pe[(size_t)(k0 + j) * a.dr + lane + 32 * (c - 4)]);
-    for (int t = 16; t; t >>= 1) s += __shfl_xor_sync(~0u, s, t);
-    const float mt = fmaxf(m, s), f = m == mt ? 1.f : __expf(m - mt), p = __expf(s - mt);
-    m = mt;
-    l = l * f + p;
-    for (int c = 0; c < 4; ++c) o[c] = o[c] * f + p * bf16_to_f32(v[lane + 32 * c]);
+  const int hb = a.Hq * a.B, rest = (int)(blockIdx.x % (unsigned)hb);
+  const int qt = p.qtiles - 1 - (int)(blockIdx.x / (unsigned)hb);
+  const int b = rest / a.Hq, h = rest % a.Hq, hk = h / (a.Hq / a.Hkv);
+
+  pdl_wait();
+  pdl_launch_dependents();
+  const int q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1);
+  const int k0 = __ldg(a.kv_start + b), k1 = __ldg(a.kv_start + b + 1);
+  const bool bad_rows = q0 < 0 || q1 < q0 || q1 > a.Nq || k0 < 0 || k1 < k0 || k1 > a.Nkv || q1 - q0 > a.max_q;
+  if (bad_rows) {
+    if (tid == 0 && h == 0 && qt == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
+    return;
   }
-  for (int c = 0; c < 4; ++c)
-    a.out[((size_t)(q0 + i) * a.Hq + h) * 128 + lane + 32 * c] = f32_to_bf16_rn(seen > 0 ? o[c] / l : 0.f);
+  const int nq = q1 - q0, n_k = k1 - k0, first = qt * 2 * kRows;
+  if (first >= nq) return;
+  // key tiles that each tile of queries sees: up to its last row's last key
+  int nt[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int begin = first + w * kRows, last = min(nq, begin + kRows) - 1;  // last row
+    const long long seen = begin < nq ? (long long)last + n_k - nq + 1 : 0;
+    nt[w] = seen > 0 ? (int)((min(seen, (long long)n_k) + kRows - 1) / kRows) : 0;
+  }
+  const int tiles = max(nt[0], nt[1]);
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&q_full[w], 1);
+      mbar_init(&s_full[w], 1);
+      mbar_init(&p_full[w], 4);
+      mbar_init(&o_full[w], 1);
+    }
+    mbar_init(partial, 1);
+    mbar_init(tail, 1);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      // -------------------------------------------------------------- producer
+      if (elect_one()) {
+        const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+        const int dq = 128 + a.dr;
+        int nkl = 0, nvl = 0;  // tiles requested
+        const bool half[2] = {nt[0] > 0, nt[1] > 0};
+        auto load_q = [&](int w) {
+          mbar_arrive_expect_tx(&q_full[w], (uint32_t)p.atoms * kAtom);
+          for (int c = 0; c < p.atoms; ++c)
+            tma_load_2d(smem + (uint32_t)(w * p.atoms + c) * kAtom, &p.mq, h * dq + 64 * c, q0 + first + w * kRows,
+                        &q_full[w], once);
+        };
+        auto load_k = [&](int i, int st) {
+          uint8_t* dst = smem + lay.k + (uint32_t)(st * p.atoms) * kAtom;
+          mbar_arrive_expect_tx(&k_full[st], (uint32_t)p.atoms * kAtom);
+          tma_load_2d(dst, &p.mk, hk * 128, k0 + i * kRows, &k_full[st], keep);
+          tma_load_2d(dst + kAtom, &p.mk, hk * 128 + 64, k0 + i * kRows, &k_full[st], keep);
+          if (p.atoms > 2) tma_load_2d(dst + 2 * kAtom, &p.mp, 0, k0 + i * kRows, &k_full[st], keep);
+          ++nkl;
+        };
+        auto load_v = [&](int i, int st) {
+          uint8_t* dst = smem + lay.v + (uint32_t)(st * 2) * kAtom;
+          mbar_arrive_expect_tx(&v_full[st], 2 * kAtom);
+          tma_load_2d(dst, &p.mv, hk * 128, k0 + i * kRows, &v_full[st], keep);
+          tma_load_2d(dst + kAtom, &p.mv, hk * 128 + 64, k0 + i * kRows, &v_full[st], keep);
+          ++nvl;
+        };
+        int ks = 0, vs = 0;
+        uint32_t kp = 0, vp = 0;  // parity of the slot's current use
+        for (int i = 0; i < tiles; ++i) {
+          if (i == 0 && half[0]) load_q(0);
+          if (i >= p.nk && !mbar_wait_bounded(&k_empty[ks], kp ^ 1u, a.dev_status)) break;
+          load_k(i, ks);
+          if (i == 0 && half[1]) load_q(1);
+          if (i >= p.nv && !mbar_wait_bounded(&v_empty[vs], vp ^ 1u, a.dev_status)) break;
+          load_v(i, vs);
+          if (++ks == p.nk) ks = 0, kp ^= 1u;
+          if (++vs == p.nv) vs = 0, vp ^= 1u;
+        }
+        // every requested copy lands before the shared memory is released
+        if (tiles > 0) {
+          for (int w = 0; w < 2; ++w)
+            if (half[w]) mbar_wait_bounded(&q_full[w], 0, nullptr);
+          for (int j = max(0, nkl - p.nk); j < nkl; ++j)
+            mbar_wait_bounded(&k_full[j % p.nk], (uint32_t)((j / p.nk) & 1), nullptr);
+          for (int j = max(0, nvl - p.nv); j < nvl; ++j)
+            mbar_wait_bounded(&v_full[j % p.nv], (uint32_t)((j / p.nv) & 1), nullptr);
+        }
+      }
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- MMA issuer
+      if (tiles > 0 && elect_one()) {
+        const uint32_t id_s = idesc_bf16_f32(128, 128, false, false) | (p.negate ? 1u << 13 : 0u);
+        const uint32_t id_o = idesc_bf16_f32(128, 128, false, true);
+        const uint32_t q_addr = smem_u32(smem), k_addr = smem_u32(smem + lay.k), v_addr = smem_u32(smem + lay.v);
+        const int pe_steps = a.dr / 16;
+        bool ok = true;
+        int ks = 0, vs = 0;
+        uint32_t kp = 0, vp = 0;
+        auto issue_s = [&](int w, int st) {
+          uint64_t dq = sw128_desc(q_addr + (uint32_t)(w * p.atoms) * kAtom);
+          uint64_t dk = sw128_desc(k_addr + (uint32_t)(st * p.atoms) * kAtom);
+          const uint32_t d = tmem + (uint32_t)w * 128u;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16(d, dq + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2, dk + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2, id_s,
+                      kk > 0);
+          dq += 2 * (kAtom >> 4);
+          dk += 2 * (kAtom >> 4);
+          for (int kk = 0; kk < pe_steps; ++kk) umma_bf16(d, dq + 2 * kk, dk + 2 * kk, id_s, 1);
+          umma_commit(&s_full[w]);
+        };
+        ok = mbar_wait_bounded(&k_full[0], 0, a.dev_status);
+        for (int w = 0; w < 2 && ok; ++w)
+          if (nt[w] > 0) {
+            ok = mbar_wait_bounded(&q_full[w], 0, a.dev_status);
+            if (ok) {
+              tc_fence_after();
+              issue_s(w, 0);
+            }
+          }
+        if (ok) umma_commit(&k_empty[0]);
+        if (++ks == p.nk) ks = 0, kp ^= 1u;
+        for (int i = 0; ok && i < tiles; ++i) {
+          bool have_v = false, have_k = false;
+          for (int w = 0; w < 2 && ok; ++w) {
+            if (i >= nt[w]) continue;
+            if (!have_v) {
+              if (!(ok = mbar_wait_bounded(&v_full[vs], vp, a.dev_status))) break;
+              have_v = true;
+              if (i == tiles - 1 && (i + 1) * kRows > n_k) {  // rows past n_k must not be NaN
+                mbar_arrive(partial);
+                if (!(ok = mbar_wait_bounded(tail, 0, a.dev_status))) break;
+              }
+            }
+            if (!(ok = mbar_wait_bounded(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
+            tc_fence_after();
+            const uint64_t dv = sw128_mn_desc(v_addr + (uint32_t)(vs * 2) * kAtom, kAtom);
+            const uint32_t d = tmem + kOCol + (uint32_t)w * 128u, pa = tmem + (uint32_t)w * 128u;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) umma_bf16_ts(d, pa + kk * 8, dv + kk * 128, id_o, i > 0 || kk > 0);
+            if (i == nt[w] - 1) umma_commit(&o_full[w]);
+            if (i + 1 < nt[w]) {
+              if (!have_k) {
+                if (!(ok = mbar_wait_bounded(&k_full[ks], kp, a.dev_status))) break;
+                have_k = true;
+                tc_fence_after();
+              }
+              issue_s(w, ks);
+            }
+          }
+          if (!ok) break;
+          umma_commit(&v_empty[vs]);
+          if (++vs == p.nv) vs = 0, vp ^= 1u;
+          if (have_k) {
+            umma_commit(&k_empty[ks]);
+            if (++ks == p.nk) ks = 0, kp ^= 1u;
+          }
+        }
+        // products left by a timeout get a bounded chance to finish; on the normal path this is
+        // the end of the last one
+        umma_commit(drain);
+        mbar_wait_bounded(drain, 0, nullptr);
+      }
+    } else if (warp == 2) {
+      // -------------------------------------------------------------- value rows past n_k
+      if (tiles > 0 && tiles * kRows > n_k) {
+        const uint64_t since = global_timer_ns();
+        bool got = mbar_try_wait(partial, 0);
+        while (!got && global_timer_ns() - since < 8 * kWaitLimitNs) got = mbar_try_wait(partial, 0);
+        if (__all_sync(~0u, got)) {
+          const int valid = n_k - (tiles - 1) * kRows;
+          uint8_t* v = smem + lay.v + (uint32_t)((tiles - 1) % p.nv * 2) * kAtom;
+          for (int c = 0; c < 2; ++c)
+            for (int e = valid * 8 + lane; e < kRows * 8; e += 32)
+              *reinterpret_cast<uint4*>(v + c * kAtom + e * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tail);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int w = (warp - 4) >> 2, quad = warp & 3;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_col = tmem + lanes + (uint32_t)w * 128u, o_col = tmem + lanes + kOCol + (uint32_t)w * 128u;
+    const int row = first + w * kRows + quad * 32 + lane;  // the thread's query
+    const int shift = n_k - nq;
+    const int seen = (int)max(0LL, min((long long)n_k, (long long)row + shift + 1));  // keys it sees
+    // keys that every row of the warp sees (rows past n_q see no fewer)
+    const int all = __shfl_sync(~0u, seen, 0);
+    const uint64_t scale2 = pack2(p.scale2, p.scale2);
+    float m = kFloor;
+    uint64_t l0 = 0, l1 = 0;
+    bool ok = true;
+    for (int i = 0; i < nt[w]; ++i) {
+      ok = __all_sync(~0u, mbar_wait_bounded(&s_full[w], (uint32_t)(i & 1), a.dev_status));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, s[c]);
+      tmem_wait_ld();
+      const int lim = seen - i * kRows;
+      const bool masked = all < (i + 1) * kRows;
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * c + e >= lim) s[c][e] = __float_as_uint(-3e38f);
+      }
+      float t[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        t[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int e = 1; e < 32; ++e) t[c] = fmaxf(t[c], __uint_as_float(s[c][e]));
+      }
+      const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale2, kFloor);
+      if (i == 0) {
+        m = top;
+      } else {
+        const bool move = top > m + kRescale;
+        if (__any_sync(~0u, move)) {  // rescale this warp's rows of O
+          const float f = move ? fast_exp2(m - top) : 1.f;
+          if (move) m = top;
+          const uint64_t f2 = pack2(f, f);
+          l0 = fma2(l0, f2, 0);
+          l1 = fma2(l1, f2, 0);
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(o_col + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+            tmem_st16(o_col + c, v);
+          }
+        }
+      }
+      const uint64_t m2 = pack2(-m, -m);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w16[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint64_t x =
+              fma2(((uint64_t)s[c][2 * e + 1] << 32) | s[c][2 * e], scale2, m2);
+          float lo = fast_exp2(lo_of(x)), hi = fast_exp2(hi_of(x));
+          if (masked) {
+            lo = 32 * c + 2 * e < lim ? lo : 0.f;
+            hi = 32 * c + 2 * e + 1 < lim ? hi : 0.f;
+          }
+          if (e & 1) l1 = add2(l1, pack2(lo, hi));
+          else l0 = add2(l0, pack2(lo, hi));
+          w16[e] = pack_bf16x2_rn(lo, hi);
+        }
+        tmem_st16(s_col + 16 * c, w16);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[w]);
+    }
+    // the output: zeros for a row that sees no key
+    if (ok && nt[w] > 0) ok = __all_sync(~0u, mbar_wait_bounded(&o_full[w], 0, a.dev_status));
+    if (ok) {
+      tc_fence_after();
+      const uint64_t ls = add2(l0, l1);
+      const float inv = seen > 0 ? 1.f / (lo_of(ls) + hi_of(ls)) : 0.f;
+      uint16_t* out = a.out + ((size_t)(q0 + row) * a.Hq + h) * 128;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t v[32];
+        if (nt[w] > 0) {
+          tmem_ld32(o_col + c, v);
+          tmem_wait_ld();
+        }
+        if (row < nq) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (seen > 0) {
+              x.x = pack_bf16x2_rn(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
+              x.y = pack_bf16x2_rn(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+              x.z = pack_bf16x2_rn(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
+              x.w = pack_bf16x2_rn(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
+            }
+            *reinterpret_cast<uint4*>(out + c + e) = x;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
-  stief_prefill_kernel<<<dim3((a.max_q + 3) / 4, a.Hq, a.B), 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  Args p{};
+  p.a = a;
+  p.atoms = a.dr > 0 ? 3 : 2;
+  p.nk = 2;
+  p.nv = a.dr > 0 ? 1 : 2;  // (three atoms of keys leave room for one value tile)
+  p.qtiles = (a.max_q + 2 * kRows - 1) / (2 * kRows);
+  p.scale2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
+  p.negate = a.scale < 0;
+  const long long blocks = (long long)p.qtiles * a.Hq * a.B;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const uint32_t smem = layout_of(p.atoms, p.nk, p.nv).total;
+  const uint64_t rows = a.Nkv > 0 ? a.Nkv : 1;  // (no keys: the maps are never used)
+  const void* k = a.Nkv > 0 ? a.k : a.q;
+  const void* v = a.Nkv > 0 ? a.v : a.q;
+  const void* pe = a.Nkv > 0 && a.dr > 0 ? a.pe : a.q;
+  const uint64_t dq = (uint64_t)a.Hq * (128 + a.dr), dk = (uint64_t)a.Hkv * 128, dp = a.dr > 0 ? a.dr : 64;
+  if (!encode_tiled_bf16_2d(&p.mq, a.q, dq, (uint64_t)a.Nq, dq * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_bf16_2d(&p.mk, k, dk, rows, dk * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_bf16_2d(&p.mv, v, dk, rows, dk * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_bf16_2d(&p.mp, pe, dp, a.dr > 0 ? rows : 1, dp * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  static SmemLimit limit;
+  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_prefill_kernel), a.device, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, stief_prefill_kernel, p);
 }
 
 }  // namespace stief
