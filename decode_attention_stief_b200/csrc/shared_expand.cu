@@ -1,51 +1,383 @@
 // shared_expand.cu -- the expanded form of shared latents: keys and values of every head from
 // the cache rows, for sm_100a:  k[t][h] = c_t . W_K[h]^T,  v[t][h] = c_t . W_V[h]^T.
-// This kernel: a CTA takes 16 tokens and 256 outputs, fp32 sums in order.
+//
+// A matrix product of [tokens x r] with the heads' [256 x r] weights (W_K[h] over W_V[h]).  What
+// bounds it: 4 r H 128 operations a token on the tensor cores, or, for small r, the 512 H bytes
+// a token that it writes.
+//
+// A unit is 128 tokens of one sequence x one head: one accumulator of 128 x 256 in TMEM, two of
+// them in turn.  Units are dealt out evenly, in order, heads innermost: a CTA keeps its 128 rows
+// in shared memory (two row tiles where they fit) and streams the weights' 64-column chunks
+// through a ring, so a unit costs one pass over its head's weights from L2.
+//   warp 0: TMA producer; warp 1: MMA issuer (M = 128, N = 256); warps 4-7 store the keys,
+//   warps 8-11 the values, a thread a token: 32-byte stores, so that every store fills whole
+//   sectors (16-byte stores if an output is not 32-byte aligned).  The unit of head 0 also copies
+//   the position values.
+// Row tiles begin at multiples of 128 tokens of their sequence, hence at multiples of 64 rows of
+// a page: two copies bring 64 rows each.
 #include <cstdint>
 
 #include "shared_latent.h"
 #include "stief_device.cuh"
+#include "umma.cuh"
 
 namespace stief {
 
-__global__ void __launch_bounds__(256) stief_shared_expand_kernel(const SharedExpandArgs a) {
-  __shared__ float rows[16][512];
-  const int tid = threadIdx.x, t0 = blockIdx.x * 16, w = a.r + a.dr;
-  const int end = min(a.N, a.kv_start[a.B]);
-  if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && a.kv_start[a.B] > a.N) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
-  for (int t = 0; t < 16; ++t) {
-    const int i = t0 + t;
-    if (i >= end) break;
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.kv_start[mid] <= i) lo = mid;
-      else hi = mid;
+namespace {
+
+constexpr int kRows = 128;                  // tokens a unit
+constexpr uint32_t kAtomA = kRows * 128;    // 128 rows x 64 columns
+constexpr uint32_t kStageB = 256 * 128;     // 256 weight rows x 64 columns
+constexpr int kThreads = 384;
+constexpr int kMaxStages = 6;
+constexpr uint32_t kTmemCols = 512;
+
+struct Args {
+  CUtensorMap mc;        // pool [rows][w], box 64 x 64
+  CUtensorMap mwk, mwv;  // W [H * 128][r], box 64 x 128
+  SharedExpandArgs a;
+  int chunks, na, nb;    // 64-column chunks of r, row tiles and weight chunks held
+  int wide;              // outputs are 32-byte aligned
+};
+
+struct Layout {
+  uint32_t b, bars, total;
+};
+__host__ __device__ inline Layout layout_of(int chunks, int na, int nb) {
+  Layout l;
+  l.b = (uint32_t)(na * chunks) * kAtomA;
+  l.bars = l.b + (uint32_t)nb * kStageB;
+  l.total = l.bars + 8 * (2 * kMaxStages + 12);
+  return l;
+}
+
+// Rows [s0, s1) of sequence b (none if kv_start is not ascending from 0 within the outputs).
+__device__ __forceinline__ void rows_of(const SharedExpandArgs& a, int b, int& s0, int& s1) {
+  s0 = __ldg(a.kv_start + b);
+  s1 = min(__ldg(a.kv_start + b + 1), a.N);
+  if (s0 < 0 || s1 < s0) s1 = s0 = 0;
+}
+
+struct Unit {
+  int b, j, h;         // sequence, row tile of it, head
+  int s0, len;         // first output row, rows of the sequence
+  bool new_tile, last_of_tile;
+};
+// Walks a CTA's units; every warp role walks the same way.
+struct Walk {
+  const SharedExpandArgs& a;
+  int b, j, h;
+  long long left;
+  bool fresh = true;
+  __device__ bool next(Unit& u) {
+    while (left > 0 && b < a.B) {
+      int s0, s1;
+      rows_of(a, b, s0, s1);
+      const int n = (s1 - s0 + kRows - 1) / kRows;
+      if (j >= n) {
+        j = 0;
+        h = 0;
+        ++b;
+        continue;
+      }
+      u.b = b;
+      u.j = j;
+      u.h = h;
+      u.s0 = s0;
+      u.len = s1 - s0;
+      u.new_tile = fresh || h == 0;
+      fresh = false;
+      --left;
+      if (++h == a.H) {
+        h = 0;
+        ++j;
+      }
+      u.last_of_tile = h == 0 || left == 0;
+      return true;
     }
-    const int pos = i - a.kv_start[lo], pi = pos / a.page_size;
-    const int page = pi < a.max_pages ? a.block_table[(size_t)lo * a.max_pages + pi] : -1;
-    const bool mapped = page >= 0 && page < a.num_pages;
-    const uint16_t* src = a.pages + ((size_t)(mapped ? page : 0) * a.page_size + pos % a.page_size) * w;
-    for (int c = tid; c < a.r; c += 256) rows[t][c] = mapped ? bf16_to_f32(src[c]) : 0.f;
-    if (blockIdx.y == 0)
-      for (int c = tid; c < a.dr; c += 256) a.pe[(size_t)i * a.dr + c] = mapped ? src[a.r + c] : (uint16_t)0;
+    return false;
+  }
+};
+
+struct Ring {
+  int n, st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == n) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const __grid_constant__ Args p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int warp_sum[kThreads / 32], start_b, start_j;
+  const SharedExpandArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Layout lay = layout_of(p.chunks, p.na, p.nb);
+  uint64_t* b_full = reinterpret_cast<uint64_t*>(smem + lay.bars);
+  uint64_t* b_empty = b_full + kMaxStages;
+  uint64_t* a_full = b_empty + kMaxStages;  // [2]
+  uint64_t* a_empty = a_full + 2;           // [2]
+  uint64_t* d_full = a_full + 4;            // [2] an accumulator is complete
+  uint64_t* d_empty = a_full + 6;           // [2] it has been read
+  uint64_t* drain = a_full + 8;
+
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&a_full[i], 1);
+      mbar_init(&a_empty[i], 1);
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 8);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    prefetch_tensormap(&p.mc);
+    prefetch_tensormap(&p.mwk);
+    prefetch_tensormap(&p.mwv);
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
+
+  pdl_wait();
+  pdl_launch_dependents();
+  // where this CTA's units begin: a prefix sum of the sequences' row tiles
+  const int per_thread = (a.B + kThreads - 1) / kThreads, c0 = min(a.B, tid * per_thread), c1 = min(a.B, c0 + per_thread);
+  int sum = 0;
+  for (int b = c0; b < c1; ++b) {
+    int s0, s1;
+    rows_of(a, b, s0, s1);
+    sum += (s1 - s0 + kRows - 1) / kRows;
+    if (blockIdx.x == 0 && (s0 != __ldg(a.kv_start + b) || s1 != __ldg(a.kv_start + b + 1)))
+      report(a.dev_status, STIEF_DEV_BAD_LENGTH);
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int total_tiles = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i == warp) incl += total_tiles;
+    total_tiles += warp_sum[i];
+  }
+  const long long total = (long long)total_tiles * a.H, per = (total + gridDim.x - 1) / gridDim.x;
+  const long long u0 = (long long)blockIdx.x * per;
+  const long long count = u0 >= total ? 0 : min(per, total - u0);
+  const int tile0 = (int)(u0 / a.H);
+  if (count > 0 && tile0 >= incl - sum && tile0 < incl) {
+    int at = incl - sum, b = c0;
+    for (;; ++b) {
+      int s0, s1;
+      rows_of(a, b, s0, s1);
+      const int n = (s1 - s0 + kRows - 1) / kRows;
+      if (tile0 < at + n) break;
+      at += n;
+    }
+    start_b = b;
+    start_j = tile0 - at;
   }
   __syncthreads();
-  const int h = blockIdx.y;
-  const uint16_t* W = (tid < 128 ? a.W_K : a.W_V) + ((size_t)h * 128 + (tid & 127)) * a.r;
-  float acc[16] = {};
-  for (int c = 0; c < a.r; ++c) {
-    const float x = bf16_to_f32(W[c]);
-    for (int t = 0; t < 16; ++t) acc[t] += x * rows[t][c];
+  const uint32_t tmem = tmem_slot;
+  Walk walk{a, count > 0 ? start_b : 0, count > 0 ? start_j : 0, (int)(u0 - (long long)tile0 * a.H), count};
+  Unit u;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    if (elect_one()) {
+      const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+      Ring ra{p.na}, rb{p.nb};
+      int na = 0, nb = 0;  // tiles and chunks requested
+      bool ok = true;
+      while (ok && walk.next(u)) {
+        if (u.new_tile) {
+          if (na >= p.na && !(ok = mbar_wait_bounded(&a_empty[ra.st], ra.ph ^ 1u, a.dev_status))) break;
+          mbar_arrive_expect_tx(&a_full[ra.st], (uint32_t)p.chunks * kAtomA);
+          uint8_t* dst = smem + (uint32_t)(ra.st * p.chunks) * kAtomA;
+          for (int half = 0; half < 2; ++half) {
+            const int pos = u.j * kRows + half * 64, pi = pos / a.page_size;
+            const int page = pos < u.len && pi < a.max_pages ? __ldg(a.block_table + (size_t)u.b * a.max_pages + pi) : -1;
+            // rows past the pool read as zeros: so do those of a page that is not mapped
+            const int row = page >= 0 && page < a.num_pages ? page * a.page_size + pos % a.page_size
+                                                            : a.num_pages * a.page_size;
+            for (int c = 0; c < p.chunks; ++c)
+              tma_load_2d(dst + (uint32_t)c * kAtomA + half * (kAtomA / 2), &p.mc, 64 * c, row, &a_full[ra.st], once);
+          }
+          ++na;
+          ra.next();
+        }
+        for (int c = 0; c < p.chunks; ++c, ++nb, rb.next()) {
+          if (nb >= p.nb && !(ok = mbar_wait_bounded(&b_empty[rb.st], rb.ph ^ 1u, a.dev_status))) break;
+          uint8_t* dst = smem + lay.b + (uint32_t)rb.st * kStageB;
+          mbar_arrive_expect_tx(&b_full[rb.st], kStageB);
+          tma_load_2d(dst, &p.mwk, 64 * c, u.h * 128, &b_full[rb.st], keep);
+          tma_load_2d(dst + kStageB / 2, &p.mwv, 64 * c, u.h * 128, &b_full[rb.st], keep);
+        }
+      }
+      // every requested copy lands before the shared memory is released
+      for (int k = max(0, na - p.na); k < na; ++k)
+        mbar_wait_bounded(&a_full[k % p.na], (uint32_t)((k / p.na) & 1), nullptr);
+      for (int k = max(0, nb - p.nb); k < nb; ++k)
+        mbar_wait_bounded(&b_full[k % p.nb], (uint32_t)((k / p.nb) & 1), nullptr);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (elect_one()) {
+      const uint32_t id = idesc_bf16_f32(128, 256, false, false);
+      const uint32_t a_addr = smem_u32(smem), b_addr = smem_u32(smem + lay.b);
+      Ring ra{p.na}, rb{p.nb};
+      uint32_t d = 0, dp = 0;  // accumulator, parity of its use
+      int n = 0, st_a = 0;
+      bool ok = true;
+      while (ok && walk.next(u)) {
+        if (u.new_tile) {
+          if (!(ok = mbar_wait_bounded(&a_full[ra.st], ra.ph, a.dev_status))) break;
+          st_a = ra.st;
+          ra.next();
+        }
+        if (n >= 2 && !(ok = mbar_wait_bounded(&d_empty[d], dp ^ 1u, a.dev_status))) break;
+        uint64_t da = sw128_desc(a_addr + (uint32_t)(st_a * p.chunks) * kAtomA);
+        for (int c = 0; c < p.chunks; ++c, rb.next(), da += kAtomA >> 4) {
+          if (!(ok = mbar_wait_bounded(&b_full[rb.st], rb.ph, a.dev_status))) break;
+          tc_fence_after();
+          const uint64_t db = sw128_desc(b_addr + (uint32_t)rb.st * kStageB);
+          const int steps = min(4, (a.r - 64 * c) / 16);
+          const uint32_t acc = tmem + d * 256u;
+          umma_bf16(acc, da, db, id, c > 0);
+          if (steps > 1) umma_bf16(acc, da + 2, db + 2, id, 1);
+          if (steps > 2) umma_bf16(acc, da + 4, db + 4, id, 1);
+          if (steps > 3) umma_bf16(acc, da + 6, db + 6, id, 1);
+          umma_commit(&b_empty[rb.st]);
+        }
+        if (!ok) break;
+        if (u.last_of_tile) umma_commit(&a_empty[st_a]);
+        umma_commit(&d_full[d]);
+        d ^= 1u;
+        if (d == 0) dp ^= 1u;
+        ++n;
+      }
+      // (on the normal path the end of the last product, after a timeout a bounded chance to finish)
+      umma_commit(drain);
+      mbar_wait_bounded(drain, 0, nullptr);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- output
+    const int half = (warp - 4) >> 2, quad = warp & 3;  // 0: keys, 1: values
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    uint16_t* const base = half ? a.v : a.k;
+    uint32_t d = 0, dp = 0;
+    while (walk.next(u)) {
+      const int t = u.j * kRows + quad * 32 + lane;  // token of the sequence
+      const bool live = t < u.len;
+      if (u.h == 0 && half == 0 && a.dr > 0 && live) {
+        const int pi = t / a.page_size;
+        const int page = pi < a.max_pages ? __ldg(a.block_table + (size_t)u.b * a.max_pages + pi) : -1;
+        const bool mapped = page >= 0 && page < a.num_pages;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.pages + ((size_t)(mapped ? page : 0) * a.page_size + t % a.page_size) * (a.r + a.dr) + a.r);
+        uint4* dst = reinterpret_cast<uint4*>(a.pe + (size_t)(u.s0 + t) * a.dr);
+        for (int c = 0; c < a.dr / 8; ++c) dst[c] = mapped ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+      }
+      if (!__all_sync(~0u, mbar_wait_bounded(&d_full[d], dp, a.dev_status))) break;
+      tc_fence_after();
+      uint16_t* out = base + ((size_t)(u.s0 + t) * a.H + u.h) * 128;
+      const uint32_t col = tmem + lanes + d * 256u + (uint32_t)half * 128u;
+#pragma unroll
+      for (int c = 0; c < 128; c += 64) {
+        uint32_t x[2][32];
+        tmem_ld32(col + c, x[0]);
+        tmem_ld32(col + c + 32, x[1]);
+        tmem_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 64; e += 16) {
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              y[i] = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 2 * i]),
+                                    __uint_as_float(x[e >> 5][(e & 31) + 2 * i + 1]));
+            store32(out + c + e, y, p.wide);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_empty[d]);
+      d ^= 1u;
+      if (d == 0) dp ^= 1u;
+    }
   }
-  uint16_t* dst = tid < 128 ? a.k : a.v;
-  for (int t = 0; t < 16; ++t)
-    if (t0 + t < end) dst[((size_t)(t0 + t) * a.H + h) * 128 + (tid & 127)] = f32_to_bf16_rn(acc[t]);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 cudaError_t launch_shared_expand(const SharedExpandArgs& a, cudaStream_t stream) {
-  stief_shared_expand_kernel<<<dim3((a.N + 15) / 16, a.H), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  Args p{};
+  p.a = a;
+  p.chunks = (a.r + 63) / 64;
+  p.wide = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 31u) == 0;
+  // two row tiles where at least three weight chunks fit beside them
+  constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
+  p.nb = 3;
+  p.na = layout_of(p.chunks, 2, p.nb).total <= kMost ? 2 : 1;
+  while (p.nb < kMaxStages && layout_of(p.chunks, p.na, p.nb + 1).total <= kMost) ++p.nb;
+  uint32_t smem = layout_of(p.chunks, p.na, p.nb).total;
+  if (smem > kMost) return cudaErrorInvalidValue;
+  if (smem < 120u * 1024u) smem = 120u * 1024u;  // one CTA an SM: it holds all of TMEM
+  const uint64_t w = (uint64_t)(a.r + a.dr), r = (uint64_t)a.r;
+  if (!encode_tiled_bf16_2d(&p.mc, a.pages, w, (uint64_t)a.num_pages * a.page_size, w * 2, 64, 64,
+                            CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_bf16_2d(&p.mwk, a.W_K, r, (uint64_t)a.H * 128, r * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_bf16_2d(&p.mwv, a.W_V, r, (uint64_t)a.H * 128, r * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  static SmemLimit limit;
+  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_shared_expand_kernel), a.device, (int)smem);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than there can be units
+  const long long most = ((long long)a.N / kRows + a.B) * a.H;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(most < a.sms ? most : a.sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, stief_shared_expand_kernel, p);
 }
 
 }  // namespace stief
