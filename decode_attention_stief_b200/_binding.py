@@ -55,6 +55,8 @@ def library_path() -> str:
 def library() -> ctypes.CDLL:
     """Load libstief.so (once).  Raises StiefError if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -859,22 +861,36 @@ def plan_workspace(device="cuda") -> torch.Tensor:
     return torch.zeros(stief_plan_workspace_bytes(), dtype=torch.uint8, device=device)
 
 
-def _ws(workspace):
+# The calls below cost the host several microseconds of Python each, which a decode step pays
+# many times over, so their checks take the short way when everything is as it should be: one
+# test a tensor, and the long way (which says what is wrong) only when it fails.
+
+def _here(t, name, dtype, ndim, dev):
+    """Data pointer of a contiguous `ndim`-dimensional tensor of `dtype` on device `dev`, the
+    current one: the library launches there."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.get_device() == dev \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, dtype, ndim)
+    raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _ws(workspace, dev):
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on the current device (cuda:{dev}), got {workspace.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _opt(t, name, dtype, ndim):
-    return None if t is None else _dev(t, name, dtype, ndim)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _one_device(*tensors):
-    """The tensors' device must be the current one: the library launches there."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensors must be on the current device (cuda:{cur}), got {t.device}")
+def _stream_on(stream, dev):
+    """The stream given, or device `dev`'s current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream_ptr(stream)
 
 
 def stief_plan_pages(new_tokens, seq_lens, block_table, free_pages, free_count, slots, q_start,
@@ -887,42 +903,46 @@ def stief_plan_pages(new_tokens, seq_lens, block_table, free_pages, free_count, 
     kv_start [B + 1], seq_lens_out [B] (each written, or None); free_count_out [1].  All int32.
     seq_lens_out may be seq_lens and free_count_out may be free_count.
     """
-    i32 = torch.int32
-    pn, pl = _dev(new_tokens, "new_tokens", i32, 1), _dev(seq_lens, "seq_lens", i32, 1)
-    pt, pf = _dev(block_table, "block_table", i32, 2), _dev(free_pages, "free_pages", i32, 1)
-    pc, po = _dev(free_count, "free_count", i32, 1), _dev(free_count_out, "free_count_out", i32, 1)
-    ps, pq = _opt(slots, "slots", i32, 1), _opt(q_start, "q_start", i32, 1)
-    pk, pso = _opt(kv_start, "kv_start", i32, 1), _opt(seq_lens_out, "seq_lens_out", i32, 1)
-    B = new_tokens.shape[0]
-    if seq_lens.shape[0] != B or block_table.shape[0] != B or free_count.shape[0] != 1 \
-            or free_count_out.shape[0] != 1 \
-            or any(t is not None and t.shape[0] != B + 1 for t in (q_start, kv_start)) \
-            or (seq_lens_out is not None and seq_lens_out.shape[0] != B):
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    pn, pl = _here(new_tokens, "new_tokens", i32, 1, dev), _here(seq_lens, "seq_lens", i32, 1, dev)
+    pt, pf = _here(block_table, "block_table", i32, 2, dev), _here(free_pages, "free_pages", i32, 1, dev)
+    pc, po = _here(free_count, "free_count", i32, 1, dev), _here(free_count_out, "free_count_out", i32, 1, dev)
+    B, max_pages = block_table.shape
+    ps = pq = pk = pso = None
+    max_tokens, ok = 0, new_tokens.shape[0] == B == seq_lens.shape[0] and free_count.shape[0] == 1 == free_count_out.shape[0]
+    if slots is not None:
+        ps, max_tokens = _here(slots, "slots", i32, 1, dev), slots.shape[0]
+        if max_tokens == 0:
+            raise ValueError("stief_plan_pages: slots must not be empty (pass None)")
+    if q_start is not None:
+        pq, ok = _here(q_start, "q_start", i32, 1, dev), ok and q_start.shape[0] == B + 1
+    if kv_start is not None:
+        pk, ok = _here(kv_start, "kv_start", i32, 1, dev), ok and kv_start.shape[0] == B + 1
+    if seq_lens_out is not None:
+        pso, ok = _here(seq_lens_out, "seq_lens_out", i32, 1, dev), ok and seq_lens_out.shape[0] == B
+    if not ok:
         raise ValueError("stief_plan_pages: inconsistent shapes")
-    if slots is not None and slots.shape[0] == 0:
-        raise ValueError("stief_plan_pages: slots must not be empty (pass None)")
-    _one_device(new_tokens, seq_lens, block_table, free_pages, free_count, slots, q_start, kv_start,
-                seq_lens_out, free_count_out, workspace)
-    pw, nw = _ws(workspace)
+    pw, nw = _ws(workspace, dev)
     _invoke("stief_plan_pages", (pn, pl, pt, pf, pc, ps, pq, pk, pso, po, pw, nw, B,
-                                 free_pages.shape[0], int(page_size), block_table.shape[1],
-                                 0 if slots is None else slots.shape[0], _opt_status(dev_status),
-                                 _stream_ptr(stream)))
+                                 free_pages.shape[0], int(page_size), max_pages, max_tokens,
+                                 _opt_status(dev_status), _stream_on(stream, dev)))
 
 
-def _rows(t, name):
-    """Pointer and row stride of a 2-D bf16 CUDA tensor whose rows are contiguous."""
+def _rows(t, name, dev):
+    """Pointer, shape and row stride of a 2-D bf16 tensor on device `dev` whose rows are contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    n, w = t.shape
+    stride, step = t.stride()
+    if w > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return t.data_ptr(), n, w, stride if n > 1 else w
 
 
 def stief_append_shared_paged(c_new, pe_new, slots, pages,
@@ -933,18 +953,16 @@ def stief_append_shared_paged(c_new, pe_new, slots, pages,
     position part), rows contiguous, any row stride that is a multiple of 8; slots [N] int32;
     pages [num_pages][page_size][r + dr] bf16.
     """
-    pc, sc = _rows(c_new, "c_new")
-    N, r = c_new.shape
-    dr = 0 if pe_new is None else pe_new.shape[1]
-    pp, sp = _rows(pe_new, "pe_new") if dr else (None, 0)
-    psl = _dev(slots, "slots", torch.int32, 1)
-    ppg = _dev(pages, "pages", torch.bfloat16, 3)
-    if slots.shape[0] != N or pages.shape[2] != r + dr or (dr and pe_new.shape[0] != N):
+    dev = torch.cuda.current_device()
+    pc, N, r, sc = _rows(c_new, "c_new", dev)
+    pp, n_pe, dr, sp = (None, N, 0, 0) if pe_new is None else _rows(pe_new, "pe_new", dev)
+    psl = _here(slots, "slots", torch.int32, 1, dev)
+    ppg = _here(pages, "pages", torch.bfloat16, 3, dev)
+    num_pages, page_size, w = pages.shape
+    if slots.shape[0] != N or w != r + dr or n_pe != N:
         raise ValueError("stief_append_shared_paged: inconsistent shapes")
-    _one_device(c_new, pe_new, slots, pages)
-    _invoke("stief_append_shared_paged", (pc, pp, psl, ppg, N, r, dr, sc, sp, pages.shape[0],
-                                          pages.shape[1], _opt_status(dev_status),
-                                          _stream_ptr(stream)))
+    _invoke("stief_append_shared_paged", (pc, pp if dr else None, psl, ppg, N, r, dr, sc, sp, num_pages,
+                                          page_size, _opt_status(dev_status), _stream_on(stream, dev)))
 
 
 def stief_decode_shared_workspace_bytes(B: int, Hq: int, r: int) -> int:
@@ -968,20 +986,20 @@ def stief_decode_shared_paged(q, pages, block_table, seq_lens, out, workspace, m
     q [B][Hq][r + dr], pages [num_pages][page_size][r + dr], out [B][Hq][r] (written), bf16;
     block_table [B][max_pages], seq_lens [B] int32; workspace from shared_workspace_for.
     """
-    pq, ppg = _dev(q, "q", torch.bfloat16, 3), _dev(pages, "pages", torch.bfloat16, 3)
-    pt, psl = _dev(block_table, "block_table", torch.int32, 2), _dev(seq_lens, "seq_lens", torch.int32, 1)
-    po = _dev(out, "out", torch.bfloat16, 3)
+    dev, b16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
+    pq, ppg = _here(q, "q", b16, 3, dev), _here(pages, "pages", b16, 3, dev)
+    pt, psl = _here(block_table, "block_table", i32, 2, dev), _here(seq_lens, "seq_lens", i32, 1, dev)
+    po = _here(out, "out", b16, 3, dev)
     B, Hq, w = q.shape
-    r = out.shape[2]
-    if pages.shape[2] != w or tuple(out.shape) != (B, Hq, r) or r > w or block_table.shape[0] != B \
-            or seq_lens.shape[0] != B:
+    Bo, Ho, r = out.shape
+    num_pages, page_size, wp = pages.shape
+    Bt, max_pages = block_table.shape
+    if wp != w or r > w or Ho != Hq or not Bo == Bt == B == seq_lens.shape[0]:
         raise ValueError("stief_decode_shared_paged: inconsistent shapes")
-    _one_device(q, pages, block_table, seq_lens, out, workspace)
-    pw, nw = _ws(workspace)
-    _invoke("stief_decode_shared_paged", (pq, ppg, pt, psl, po, pw, nw, B, Hq, r, w - r,
-                                          pages.shape[0], pages.shape[1], block_table.shape[1],
-                                          int(max_seq_len), float(scale), _opt_status(dev_status),
-                                          _stream_ptr(stream)))
+    pw, nw = _ws(workspace, dev)
+    _invoke("stief_decode_shared_paged", (pq, ppg, pt, psl, po, pw, nw, B, Hq, r, w - r, num_pages,
+                                          page_size, max_pages, int(max_seq_len), float(scale),
+                                          _opt_status(dev_status), _stream_on(stream, dev)))
     return out
 
 
@@ -994,22 +1012,22 @@ def stief_expand_shared_paged(pages, block_table, kv_start, W_K, W_V, k, v, k_pe
     (None, or with dr = 0, for rows without a position part) bf16; block_table [B][max_pages],
     kv_start [B + 1] int32.
     """
-    ppg, pt = _dev(pages, "pages", torch.bfloat16, 3), _dev(block_table, "block_table", torch.int32, 2)
-    pst = _dev(kv_start, "kv_start", torch.int32, 1)
-    pwk, pwv = _dev(W_K, "W_K", torch.bfloat16, 3), _dev(W_V, "W_V", torch.bfloat16, 3)
-    pk, pv = _dev(k, "k", torch.bfloat16, 3), _dev(v, "v", torch.bfloat16, 3)
+    dev, b16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
+    ppg, pt = _here(pages, "pages", b16, 3, dev), _here(block_table, "block_table", i32, 2, dev)
+    pst = _here(kv_start, "kv_start", i32, 1, dev)
+    pwk, pwv = _here(W_K, "W_K", b16, 3, dev), _here(W_V, "W_V", b16, 3, dev)
+    pk, pv = _here(k, "k", b16, 3, dev), _here(v, "v", b16, 3, dev)
     H, d, r = W_K.shape
-    N, B = k.shape[0], block_table.shape[0]
-    dr = pages.shape[2] - r
-    ppe = _dev(k_pe, "k_pe", torch.bfloat16, 2) if dr > 0 and k_pe is not None else None
-    if dr < 0 or tuple(W_V.shape) != (H, d, r) or tuple(k.shape) != (N, H, d) \
-            or tuple(v.shape) != (N, H, d) or kv_start.shape[0] != B + 1 \
-            or (dr > 0 and (k_pe is None or tuple(k_pe.shape) != (N, dr))):
+    B, max_pages = block_table.shape
+    num_pages, page_size, w = pages.shape
+    N, dr = k.shape[0], w - r
+    ppe = _here(k_pe, "k_pe", b16, 2, dev) if dr > 0 and k_pe is not None else None
+    if dr < 0 or W_V.shape != W_K.shape or k.shape != (N, H, d) or v.shape != k.shape \
+            or kv_start.shape[0] != B + 1 or (dr > 0 and (k_pe is None or k_pe.shape != (N, dr))):
         raise ValueError("stief_expand_shared_paged: inconsistent shapes")
-    _one_device(pages, block_table, kv_start, W_K, W_V, k, v, k_pe)
     _invoke("stief_expand_shared_paged", (ppg, pt, pst, pwk, pwv, pk, pv, ppe, B, N, H, d, r, dr,
-                                          pages.shape[0], pages.shape[1], block_table.shape[1],
-                                          _opt_status(dev_status), _stream_ptr(stream)))
+                                          num_pages, page_size, max_pages, _opt_status(dev_status),
+                                          _stream_on(stream, dev)))
 
 
 def stief_prefill_attention(q, k, v, q_start, kv_start, out, max_q_len: int, scale: float,
@@ -1021,19 +1039,21 @@ def stief_prefill_attention(q, k, v, q_start, kv_start, out, max_q_len: int, sca
     q [Nq][Hq][d + dr], k and v [Nkv][Hkv][d], k_pe [Nkv][dr] (None when dr = 0), out
     [Nq][Hq][d] (written), bf16; q_start, kv_start [B + 1] int32.
     """
-    pq, pk = _dev(q, "q", torch.bfloat16, 3), _dev(k, "k", torch.bfloat16, 3)
-    pv, po = _dev(v, "v", torch.bfloat16, 3), _dev(out, "out", torch.bfloat16, 3)
-    pqs, pks = _dev(q_start, "q_start", torch.int32, 1), _dev(kv_start, "kv_start", torch.int32, 1)
-    ppe = _opt(k_pe, "k_pe", torch.bfloat16, 2)
+    dev, b16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
+    pq, pk = _here(q, "q", b16, 3, dev), _here(k, "k", b16, 3, dev)
+    pv, po = _here(v, "v", b16, 3, dev), _here(out, "out", b16, 3, dev)
+    pqs, pks = _here(q_start, "q_start", i32, 1, dev), _here(kv_start, "kv_start", i32, 1, dev)
     Nq, Hq, dq = q.shape
     Nkv, Hkv, d = k.shape
-    dr = 0 if k_pe is None else k_pe.shape[1]
-    if tuple(v.shape) != (Nkv, Hkv, d) or dq != d + dr or tuple(out.shape) != (Nq, Hq, d) \
-            or q_start.shape[0] != kv_start.shape[0] or (k_pe is not None and k_pe.shape[0] != Nkv):
+    ppe, n_pe, dr = None, Nkv, 0
+    if k_pe is not None:
+        ppe = _here(k_pe, "k_pe", b16, 2, dev)
+        n_pe, dr = k_pe.shape
+    B = q_start.shape[0] - 1
+    if v.shape != k.shape or dq != d + dr or out.shape != (Nq, Hq, d) or kv_start.shape[0] != B + 1 \
+            or n_pe != Nkv:
         raise ValueError("stief_prefill_attention: inconsistent shapes")
-    _one_device(q, k, v, q_start, kv_start, out, k_pe)
-    _invoke("stief_prefill_attention", (pq, pk, pv, ppe if dr else None, pqs, pks, po,
-                                        q_start.shape[0] - 1, Hq, Hkv, d, dr, Nq, Nkv,
-                                        int(max_q_len), float(scale), _opt_status(dev_status),
-                                        _stream_ptr(stream)))
+    _invoke("stief_prefill_attention", (pq, pk, pv, ppe if dr else None, pqs, pks, po, B, Hq, Hkv, d, dr,
+                                        Nq, Nkv, int(max_q_len), float(scale), _opt_status(dev_status),
+                                        _stream_on(stream, dev)))
     return out
