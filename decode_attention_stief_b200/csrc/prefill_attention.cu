@@ -38,30 +38,37 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;            // S_w at 128 w, O_w at 256 + 128 w
 constexpr float kRescale = 8.f;
 constexpr float kFloor = -1e30f;
-constexpr int kMaxSlots = 3;
+constexpr int kKeySlots = 2;
+constexpr int kMaxHalves = 6;
+constexpr uint32_t kKeys = 2 * kAtom;      // bytes of a key tile without the position part
+constexpr uint32_t kHalf = kAtom;          // bytes of 64 value rows (two atoms of 64 columns)
 
 struct Args {
   CUtensorMap mq;   // q [Nq][Hq * (128 + dr)], box 64 x 128
-  CUtensorMap mk;   // k [Nkv][Hkv * 128], box 64 x 128
-  CUtensorMap mv;   // v, same
+  CUtensorMap mk;   // k [Nkv] rows in blocks of 64 columns, box 64 x 128 x 2
+  CUtensorMap mv;   // v, box 64 x 64 x 2
   CUtensorMap mp;   // k_pe [Nkv][dr], box 64 x 128
   PrefillArgs a;
-  int atoms;        // 64-column atoms of a query or key row: 2, or 3 with a position part
-  int nk, nv;       // key and value slots
+  int atoms;        // 64-column atoms of a query row: 2, or 3 with a position part
+  int nv;           // slots of 64 value rows
   int qtiles;       // tiles of 256 queries of the longest sequence
   float scale2;     // |scale| * log2(e)
   int negate;       // scale < 0: the products are negated instead
 };
 
+// Queries (two tiles), key slots, one slot of position parts, slots of 64 value rows.  A key tile's
+// position part is wanted between its two products only, so one slot of it is enough, and what
+// that saves holds a third half tile of values: with two, the next one arrived too late.
 struct Layout {
-  uint32_t k, v, bars, total;
+  uint32_t k, pe, v, bars, total;
 };
-__host__ __device__ inline Layout layout_of(int atoms, int nk, int nv) {
+__host__ __device__ inline Layout layout_of(int atoms, int nv) {
   Layout l;
   l.k = 2u * atoms * kAtom;
-  l.v = l.k + (uint32_t)nk * atoms * kAtom;
-  l.bars = l.v + (uint32_t)nv * 2 * kAtom;
-  l.total = l.bars + 8 * (4 * kMaxSlots + 16);
+  l.pe = l.k + kKeySlots * kKeys;
+  l.v = l.pe + (uint32_t)(atoms - 2) * kAtom;
+  l.bars = l.v + (uint32_t)nv * kHalf;
+  l.total = l.bars + 8 * (2 * kKeySlots + 2 * kMaxHalves + 20);
   return l;
 }
 
@@ -88,18 +95,21 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
   __shared__ uint32_t tmem_slot;
   const PrefillArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Layout lay = layout_of(p.atoms, p.nk, p.nv);
+  const Layout lay = layout_of(p.atoms, p.nv);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + lay.bars);
-  uint64_t* k_empty = k_full + kMaxSlots;
-  uint64_t* v_full = k_empty + kMaxSlots;
-  uint64_t* v_empty = v_full + kMaxSlots;
-  uint64_t* q_full = v_empty + kMaxSlots;  // [2]
-  uint64_t* s_full = q_full + 2;           // [2] S_w of a tile is in TMEM (and O_w before it)
-  uint64_t* p_full = q_full + 4;           // [2] P_w is in TMEM
-  uint64_t* o_full = q_full + 6;           // [2] O_w is complete
-  uint64_t* partial = q_full + 8;          // the last value tile is in and is not full
-  uint64_t* tail = q_full + 9;             // its rows past n_k are cleared
-  uint64_t* drain = q_full + 10;
+  uint64_t* k_empty = k_full + kKeySlots;
+  uint64_t* v_full = k_empty + kKeySlots;
+  uint64_t* v_empty = v_full + kMaxHalves;
+  uint64_t* q_full = v_empty + kMaxHalves;  // [2]
+  uint64_t* s_full = q_full + 2;            // [2] S_w of a tile is in TMEM (and O_w before it)
+  uint64_t* p_half = q_full + 4;            // [2] P_w of the tile's first 64 keys is in TMEM
+  uint64_t* p_full = q_full + 6;            // [2] all of it
+  uint64_t* o_full = q_full + 8;            // [2] O_w is complete
+  uint64_t* partial = q_full + 10;          // the last value tile is in and is not full
+  uint64_t* tail = q_full + 11;             // its rows past n_k are cleared
+  uint64_t* drain = q_full + 12;
+  uint64_t* pe_full = q_full + 13;
+  uint64_t* pe_empty = q_full + 14;
 
   if ((smem_u32(smem) & 1023u) != 0) {
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
@@ -131,18 +141,23 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
   const int tiles = max(nt[0], nt[1]);
 
   if (tid == 0) {
-    for (int i = 0; i < kMaxSlots; ++i) {
+    for (int i = 0; i < kKeySlots; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < kMaxHalves; ++i) {
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&q_full[w], 1);
       mbar_init(&s_full[w], 1);
+      mbar_init(&p_half[w], 4);
       mbar_init(&p_full[w], 4);
       mbar_init(&o_full[w], 1);
     }
+    mbar_init(pe_full, 1);
+    mbar_init(pe_empty, 1);
     mbar_init(partial, 1);
     mbar_init(tail, 1);
     mbar_init(drain, 1);
@@ -161,49 +176,50 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
       if (elect_one()) {
         const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
         const int dq = 128 + a.dr;
-        int nkl = 0, nvl = 0;  // tiles requested
-        const bool half[2] = {nt[0] > 0, nt[1] > 0};
+        int nkl = 0, nvl = 0, npl = 0;  // tiles, halves and position parts requested
+        const bool half[2] = {nt[0] > 0, nt[1] > 0}, pos = p.atoms > 2;
         auto load_q = [&](int w) {
           mbar_arrive_expect_tx(&q_full[w], (uint32_t)p.atoms * kAtom);
           for (int c = 0; c < p.atoms; ++c)
             tma_load_2d(smem + (uint32_t)(w * p.atoms + c) * kAtom, &p.mq, h * dq + 64 * c, q0 + first + w * kRows,
                         &q_full[w], once);
         };
-        auto load_k = [&](int i, int st) {
-          uint8_t* dst = smem + lay.k + (uint32_t)(st * p.atoms) * kAtom;
-          mbar_arrive_expect_tx(&k_full[st], (uint32_t)p.atoms * kAtom);
-          tma_load_2d(dst, &p.mk, hk * 128, k0 + i * kRows, &k_full[st], keep);
-          tma_load_2d(dst + kAtom, &p.mk, hk * 128 + 64, k0 + i * kRows, &k_full[st], keep);
-          if (p.atoms > 2) tma_load_2d(dst + 2 * kAtom, &p.mp, 0, k0 + i * kRows, &k_full[st], keep);
-          ++nkl;
-        };
-        auto load_v = [&](int i, int st) {
-          uint8_t* dst = smem + lay.v + (uint32_t)(st * 2) * kAtom;
-          mbar_arrive_expect_tx(&v_full[st], 2 * kAtom);
-          tma_load_2d(dst, &p.mv, hk * 128, k0 + i * kRows, &v_full[st], keep);
-          tma_load_2d(dst + kAtom, &p.mv, hk * 128 + 64, k0 + i * kRows, &v_full[st], keep);
-          ++nvl;
-        };
         int ks = 0, vs = 0;
         uint32_t kp = 0, vp = 0;  // parity of the slot's current use
         for (int i = 0; i < tiles; ++i) {
+          const int row = k0 + i * kRows;
           if (i == 0 && half[0]) load_q(0);
-          if (i >= p.nk && !mbar_wait_bounded(&k_empty[ks], kp ^ 1u, a.dev_status)) break;
-          load_k(i, ks);
+          if (i >= kKeySlots && !mbar_wait_bounded(&k_empty[ks], kp ^ 1u, a.dev_status)) break;
+          mbar_arrive_expect_tx(&k_full[ks], kKeys);
+          tma_load_3d(smem + lay.k + (uint32_t)ks * kKeys, &p.mk, 0, row, hk * 2, &k_full[ks], keep);
+          ++nkl;
+          if (pos) {
+            if (i > 0 && !mbar_wait_bounded(pe_empty, (uint32_t)((i - 1) & 1), a.dev_status)) break;
+            mbar_arrive_expect_tx(pe_full, kAtom);
+            tma_load_2d(smem + lay.pe, &p.mp, 0, row, pe_full, keep);
+            ++npl;
+          }
           if (i == 0 && half[1]) load_q(1);
-          if (i >= p.nv && !mbar_wait_bounded(&v_empty[vs], vp ^ 1u, a.dev_status)) break;
-          load_v(i, vs);
-          if (++ks == p.nk) ks = 0, kp ^= 1u;
-          if (++vs == p.nv) vs = 0, vp ^= 1u;
+          bool ok = true;
+          for (int c = 0; c < 2 && ok; ++c) {
+            if (nvl >= p.nv && !(ok = mbar_wait_bounded(&v_empty[vs], vp ^ 1u, a.dev_status))) break;
+            mbar_arrive_expect_tx(&v_full[vs], kHalf);
+            tma_load_3d(smem + lay.v + (uint32_t)vs * kHalf, &p.mv, 0, row + 64 * c, hk * 2, &v_full[vs], keep);
+            ++nvl;
+            if (++vs == p.nv) vs = 0, vp ^= 1u;
+          }
+          if (!ok) break;
+          if (++ks == kKeySlots) ks = 0, kp ^= 1u;
         }
         // every requested copy lands before the shared memory is released
         if (tiles > 0) {
           for (int w = 0; w < 2; ++w)
-            if (half[w]) mbar_wait_bounded(&q_full[w], 0, nullptr);
-          for (int j = max(0, nkl - p.nk); j < nkl; ++j)
-            mbar_wait_bounded(&k_full[j % p.nk], (uint32_t)((j / p.nk) & 1), nullptr);
+            if (half[w] && (w == 0 || nvl > 0 || !half[0])) mbar_wait_bounded(&q_full[w], 0, nullptr);
+          for (int j = max(0, nkl - kKeySlots); j < nkl; ++j)
+            mbar_wait_bounded(&k_full[j % kKeySlots], (uint32_t)((j / kKeySlots) & 1), nullptr);
           for (int j = max(0, nvl - p.nv); j < nvl; ++j)
             mbar_wait_bounded(&v_full[j % p.nv], (uint32_t)((j / p.nv) & 1), nullptr);
+          if (npl > 0) mbar_wait_bounded(pe_full, (uint32_t)((npl - 1) & 1), nullptr);
         }
       }
     } else if (warp == 1) {
@@ -212,24 +228,35 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
         const uint32_t id_s = idesc_bf16_f32(128, 128, false, false) | (p.negate ? 1u << 13 : 0u);
         const uint32_t id_o = idesc_bf16_f32(128, 128, false, true);
         const uint32_t q_addr = smem_u32(smem), k_addr = smem_u32(smem + lay.k), v_addr = smem_u32(smem + lay.v);
+        const uint32_t pe_addr = smem_u32(smem + lay.pe);
         const int pe_steps = a.dr / 16;
         bool ok = true;
         int ks = 0, vs = 0;
         uint32_t kp = 0, vp = 0;
         auto issue_s = [&](int w, int st) {
-          uint64_t dq = sw128_desc(q_addr + (uint32_t)(w * p.atoms) * kAtom);
-          uint64_t dk = sw128_desc(k_addr + (uint32_t)(st * p.atoms) * kAtom);
+          const uint64_t dq = sw128_desc(q_addr + (uint32_t)(w * p.atoms) * kAtom);
+          const uint64_t dk = sw128_desc(k_addr + (uint32_t)st * kKeys);
           const uint32_t d = tmem + (uint32_t)w * 128u;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma_bf16(d, dq + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2, dk + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2, id_s,
                       kk > 0);
-          dq += 2 * (kAtom >> 4);
-          dk += 2 * (kAtom >> 4);
-          for (int kk = 0; kk < pe_steps; ++kk) umma_bf16(d, dq + 2 * kk, dk + 2 * kk, id_s, 1);
+          const uint64_t dqp = dq + 2 * (kAtom >> 4), dp = sw128_desc(pe_addr);
+          for (int kk = 0; kk < pe_steps; ++kk) umma_bf16(d, dqp + 2 * kk, dp + 2 * kk, id_s, 1);
           umma_commit(&s_full[w]);
         };
-        ok = mbar_wait_bounded(&k_full[0], 0, a.dev_status);
+        // keys of tile i are in
+        auto wait_k = [&](int i) -> bool {
+          return mbar_wait_bounded(&k_full[ks], kp, a.dev_status) &&
+                 (pe_steps == 0 || mbar_wait_bounded(pe_full, (uint32_t)(i & 1), a.dev_status));
+        };
+        // both products with them are issued
+        auto done_k = [&]() {
+          umma_commit(&k_empty[ks]);
+          if (pe_steps > 0) umma_commit(pe_empty);
+          if (++ks == kKeySlots) ks = 0, kp ^= 1u;
+        };
+        ok = wait_k(0);
         for (int w = 0; w < 2 && ok; ++w)
           if (nt[w] > 0) {
             ok = mbar_wait_bounded(&q_full[w], 0, a.dev_status);
@@ -238,43 +265,42 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
               issue_s(w, 0);
             }
           }
-        if (ok) umma_commit(&k_empty[0]);
-        if (++ks == p.nk) ks = 0, kp ^= 1u;
+        if (ok) done_k();
         for (int i = 0; ok && i < tiles; ++i) {
-          bool have_v = false, have_k = false;
-          for (int w = 0; w < 2 && ok; ++w) {
+          // (everything that has long arrived is waited for here, not between the products: each
+          // test of a barrier costs some hundred cycles while the products read shared memory)
+          const int va = vs, vb = vs + 1 == p.nv ? 0 : vs + 1;
+          const uint32_t pb = vb == 0 ? vp ^ 1u : vp;
+          const int last_w = i < nt[1] ? 1 : 0;
+          if (!(ok = mbar_wait_bounded(&v_full[va], vp, a.dev_status) && mbar_wait_bounded(&v_full[vb], pb, a.dev_status)))
+            break;
+          if (i == tiles - 1 && (i + 1) * kRows > n_k) {  // rows past n_k must not be NaN
+            mbar_arrive(partial);
+            if (!(ok = mbar_wait_bounded(tail, 0, a.dev_status))) break;
+          }
+          if (i + 1 < tiles && !(ok = wait_k(i + 1))) break;
+          const uint64_t dva = sw128_mn_desc(v_addr + (uint32_t)va * kHalf, kHalf / 2);
+          const uint64_t dvb = sw128_mn_desc(v_addr + (uint32_t)vb * kHalf, kHalf / 2);
+          for (int w = 0; w < 2; ++w) {
             if (i >= nt[w]) continue;
-            if (!have_v) {
-              if (!(ok = mbar_wait_bounded(&v_full[vs], vp, a.dev_status))) break;
-              have_v = true;
-              if (i == tiles - 1 && (i + 1) * kRows > n_k) {  // rows past n_k must not be NaN
-                mbar_arrive(partial);
-                if (!(ok = mbar_wait_bounded(tail, 0, a.dev_status))) break;
-              }
-            }
+            const uint32_t d = tmem + kOCol + (uint32_t)w * 128u, pa = tmem + (uint32_t)w * 128u;
+            if (!(ok = mbar_wait_bounded(&p_half[w], (uint32_t)(i & 1), a.dev_status))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(d, pa + kk * 8, dva + kk * 128, id_o, i > 0 || kk > 0);
+            if (w == last_w) umma_commit(&v_empty[va]);
             if (!(ok = mbar_wait_bounded(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
             tc_fence_after();
-            const uint64_t dv = sw128_mn_desc(v_addr + (uint32_t)(vs * 2) * kAtom, kAtom);
-            const uint32_t d = tmem + kOCol + (uint32_t)w * 128u, pa = tmem + (uint32_t)w * 128u;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) umma_bf16_ts(d, pa + kk * 8, dv + kk * 128, id_o, i > 0 || kk > 0);
-            if (i == nt[w] - 1) umma_commit(&o_full[w]);
-            if (i + 1 < nt[w]) {
-              if (!have_k) {
-                if (!(ok = mbar_wait_bounded(&k_full[ks], kp, a.dev_status))) break;
-                have_k = true;
-                tc_fence_after();
-              }
-              issue_s(w, ks);
-            }
+            for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(d, pa + 32 + kk * 8, dvb + kk * 128, id_o, 1);
+            if (i + 1 < nt[w]) issue_s(w, ks);
+            else umma_commit(&o_full[w]);
           }
           if (!ok) break;
-          umma_commit(&v_empty[vs]);
+          umma_commit(&v_empty[vb]);
           if (++vs == p.nv) vs = 0, vp ^= 1u;
-          if (have_k) {
-            umma_commit(&k_empty[ks]);
-            if (++ks == p.nk) ks = 0, kp ^= 1u;
-          }
+          if (++vs == p.nv) vs = 0, vp ^= 1u;
+          if (i + 1 < tiles) done_k();
         }
         // products left by a timeout get a bounded chance to finish; on the normal path this is
         // the end of the last one
@@ -289,10 +315,12 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
         while (!got && global_timer_ns() - since < 8 * kWaitLimitNs) got = mbar_try_wait(partial, 0);
         if (__all_sync(~0u, got)) {
           const int valid = n_k - (tiles - 1) * kRows;
-          uint8_t* v = smem + lay.v + (uint32_t)((tiles - 1) % p.nv * 2) * kAtom;
-          for (int c = 0; c < 2; ++c)
-            for (int e = valid * 8 + lane; e < kRows * 8; e += 32)
-              *reinterpret_cast<uint4*>(v + c * kAtom + e * 16) = make_uint4(0, 0, 0, 0);
+          for (int half = 0; half < 2; ++half) {
+            uint8_t* v = smem + lay.v + (uint32_t)((2 * tiles - 2 + half) % p.nv) * kHalf;
+            for (int c = 0; c < 2; ++c)
+              for (int e = max(0, valid - 64 * half) * 8 + lane; e < 64 * 8; e += 32)
+                *reinterpret_cast<uint4*>(v + c * (kHalf / 2) + e * 16) = make_uint4(0, 0, 0, 0);
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(tail);
@@ -378,6 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
           w16[e] = pack_bf16x2_rn(lo, hi);
         }
         tmem_st16(s_col + 16 * c, w16);
+        if (c == 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_half[w]);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -426,22 +460,22 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   Args p{};
   p.a = a;
   p.atoms = a.dr > 0 ? 3 : 2;
-  p.nk = 2;
-  p.nv = a.dr > 0 ? 1 : 2;  // (three atoms of keys leave room for one value tile)
+  constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
+  for (p.nv = kMaxHalves; layout_of(p.atoms, p.nv).total > kMost;) --p.nv;
   p.qtiles = (a.max_q + 2 * kRows - 1) / (2 * kRows);
   p.scale2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
   p.negate = a.scale < 0;
   const long long blocks = (long long)p.qtiles * a.Hq * a.B;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const uint32_t smem = layout_of(p.atoms, p.nk, p.nv).total;
+  const uint32_t smem = layout_of(p.atoms, p.nv).total;
   const uint64_t rows = a.Nkv > 0 ? a.Nkv : 1;  // (no keys: the maps are never used)
   const void* k = a.Nkv > 0 ? a.k : a.q;
   const void* v = a.Nkv > 0 ? a.v : a.q;
   const void* pe = a.Nkv > 0 && a.dr > 0 ? a.pe : a.q;
   const uint64_t dq = (uint64_t)a.Hq * (128 + a.dr), dk = (uint64_t)a.Hkv * 128, dp = a.dr > 0 ? a.dr : 64;
   if (!encode_tiled_bf16_2d(&p.mq, a.q, dq, (uint64_t)a.Nq, dq * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tiled_bf16_2d(&p.mk, k, dk, rows, dk * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tiled_bf16_2d(&p.mv, v, dk, rows, dk * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_bf16_3d(&p.mk, k, {64, rows, dk / 64}, {dk * 2, 128}, {64, kRows, 2}) ||
+      !encode_tiled_bf16_3d(&p.mv, v, {64, rows, dk / 64}, {dk * 2, 128}, {64, kRows / 2, 2}) ||
       !encode_tiled_bf16_2d(&p.mp, pe, dp, a.dr > 0 ? rows : 1, dp * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   static SmemLimit limit;
