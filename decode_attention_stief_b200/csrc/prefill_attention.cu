@@ -351,13 +351,12 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
       for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, s[c]);
       tmem_wait_ld();
       const int lim = seen - i * kRows;
-      const bool masked = all < (i + 1) * kRows;
-      if (masked) {
+      if (all < (i + 1) * kRows) {  // some row of the warp does not see the whole tile
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (32 * c + e >= lim) s[c][e] = __float_as_uint(-3e38f);
+            if (32 * c + e >= lim) s[c][e] = 0xff800000u;  // -inf
       }
       float t[4];
 #pragma unroll
@@ -396,11 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
         for (int e = 0; e < 16; ++e) {
           const uint64_t x =
               fma2(((uint64_t)s[c][2 * e + 1] << 32) | s[c][2 * e], scale2, m2);
-          float lo = fast_exp2(lo_of(x)), hi = fast_exp2(hi_of(x));
-          if (masked) {
-            lo = 32 * c + 2 * e < lim ? lo : 0.f;
-            hi = 32 * c + 2 * e + 1 < lim ? hi : 0.f;
-          }
+          const float lo = fast_exp2(lo_of(x)), hi = fast_exp2(hi_of(x));
           if (e & 1) l1 = add2(l1, pack2(lo, hi));
           else l0 = add2(l0, pack2(lo, hi));
           w16[e] = pack_bf16x2_rn(lo, hi);
@@ -464,6 +459,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   for (p.nv = kMaxHalves; layout_of(p.atoms, p.nv).total > kMost;) --p.nv;
   p.qtiles = (a.max_q + 2 * kRows - 1) / (2 * kRows);
   p.scale2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
+  if (p.scale2 < 1e-30f) p.scale2 = 1e-30f;  // above 0, so that a masked score stays -inf
   p.negate = a.scale < 0;
   const long long blocks = (long long)p.qtiles * a.Hq * a.B;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
