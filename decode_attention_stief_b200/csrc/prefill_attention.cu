@@ -11,11 +11,11 @@
 //     S_w = Q_w . K^T      (Q, K in shared memory, K-major, 128-byte swizzle)
 //     O_w += P_w . V       (P in tensor memory, V MN-major as it lies in memory)
 // TMEM holds S_0, S_1, O_0, O_1, 128 columns each: all of it.  P_w overwrites S_w, whose row a
-// thread holds in registers meanwhile.  The issuer alternates O_0, S_0', O_1, S_1', so that the
-// tensor cores work for one tile of queries while the softmax of the other runs.
-//   warp 0: TMA producer; warp 1: MMA issuer; warp 2: zeroes the value rows past n_k in the last
-//   tile (they may hold NaN, and 0 * NaN is NaN); warps 4-7 and 8-11: softmax of the two tiles,
-//   one thread a query row, and the output.
+// thread holds in registers meanwhile.  The tensor cores work for one tile of queries while the
+// softmax of the other runs; the product with the first 64 keys starts when half of P is there.
+//   warp 0: TMA producer; warps 1 and 3: MMA issuers of the two tiles; warp 2: zeroes the value
+//   rows past n_k in the last tile (they may hold NaN, and 0 * NaN is NaN); warps 4-7 and 8-11:
+//   softmax of the two tiles, one thread a query row, and the output.
 // The reference of the running maximum moves only when a score passes it by more than 2^8 (as in
 // the decode): a warp then rescales its own rows of O_w, whose last product is complete when S_w
 // of the next tile is, because the products run in order.
@@ -39,7 +39,8 @@ constexpr uint32_t kOCol = 256;            // S_w at 128 w, O_w at 256 + 128 w
 constexpr float kRescale = 8.f;
 constexpr float kFloor = -1e30f;
 constexpr int kKeySlots = 2;
-constexpr int kMaxHalves = 6;
+constexpr int kMaxHalves = 4;  // (no more: a tile's barrier, one of two in turn, is armed again only
+                               // after a wait for the halves of two tiles before)
 constexpr uint32_t kKeys = 2 * kAtom;      // bytes of a key tile without the position part
 constexpr uint32_t kHalf = kAtom;          // bytes of 64 value rows (two atoms of 64 columns)
 
@@ -68,7 +69,7 @@ __host__ __device__ inline Layout layout_of(int atoms, int nv) {
   l.pe = l.k + kKeySlots * kKeys;
   l.v = l.pe + (uint32_t)(atoms - 2) * kAtom;
   l.bars = l.v + (uint32_t)nv * kHalf;
-  l.total = l.bars + 8 * (2 * kKeySlots + 2 * kMaxHalves + 20);
+  l.total = l.bars + 8 * (2 * kKeySlots + 2 + kMaxHalves + 16);
   return l;
 }
 
@@ -85,6 +86,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 
@@ -98,8 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
   const Layout lay = layout_of(p.atoms, p.nv);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + lay.bars);
   uint64_t* k_empty = k_full + kKeySlots;
-  uint64_t* v_full = k_empty + kKeySlots;
-  uint64_t* v_empty = v_full + kMaxHalves;
+  uint64_t* v_full = k_empty + kKeySlots;   // [2] both halves of a value tile, tiles in turn
+  uint64_t* v_empty = v_full + 2;           // [halves]
   uint64_t* q_full = v_empty + kMaxHalves;  // [2]
   uint64_t* s_full = q_full + 2;            // [2] S_w of a tile is in TMEM (and O_w before it)
   uint64_t* p_half = q_full + 4;            // [2] P_w of the tile's first 64 keys is in TMEM
@@ -107,9 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
   uint64_t* o_full = q_full + 8;            // [2] O_w is complete
   uint64_t* partial = q_full + 10;          // the last value tile is in and is not full
   uint64_t* tail = q_full + 11;             // its rows past n_k are cleared
-  uint64_t* drain = q_full + 12;
-  uint64_t* pe_full = q_full + 13;
-  uint64_t* pe_empty = q_full + 14;
+  uint64_t* drain = q_full + 12;            // [2]
 
   if ((smem_u32(smem) & 1023u) != 0) {
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
@@ -140,27 +144,26 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
   }
   const int tiles = max(nt[0], nt[1]);
 
-  if (tid == 0) {
+  if (tid == 0 && tiles > 0) {
+    // a slot is empty when both tiles of queries have read it.  (Where one of them sees a key tile
+    // less, that is the last one, whose slot nobody waits for.)
+    const uint32_t users = (nt[0] > 0) + (nt[1] > 0);
     for (int i = 0; i < kKeySlots; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], users);
     }
-    for (int i = 0; i < kMaxHalves; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
+    for (int i = 0; i < kMaxHalves; ++i) mbar_init(&v_empty[i], users);
     for (int w = 0; w < 2; ++w) {
+      mbar_init(&v_full[w], 1);
       mbar_init(&q_full[w], 1);
       mbar_init(&s_full[w], 1);
       mbar_init(&p_half[w], 4);
       mbar_init(&p_full[w], 4);
       mbar_init(&o_full[w], 1);
+      mbar_init(&drain[w], 1);
     }
-    mbar_init(pe_full, 1);
-    mbar_init(pe_empty, 1);
-    mbar_init(partial, 1);
+    mbar_init(partial, (nt[0] == tiles) + (nt[1] == tiles));
     mbar_init(tail, 1);
-    mbar_init(drain, 1);
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
       if (elect_one()) {
         const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
         const int dq = 128 + a.dr;
-        int nkl = 0, nvl = 0, npl = 0;  // tiles, halves and position parts requested
+        int nkl = 0, nvl = 0;  // key tiles and value halves requested
         const bool half[2] = {nt[0] > 0, nt[1] > 0}, pos = p.atoms > 2;
         auto load_q = [&](int w) {
           mbar_arrive_expect_tx(&q_full[w], (uint32_t)p.atoms * kAtom);
@@ -184,128 +187,96 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
             tma_load_2d(smem + (uint32_t)(w * p.atoms + c) * kAtom, &p.mq, h * dq + 64 * c, q0 + first + w * kRows,
                         &q_full[w], once);
         };
-        int ks = 0, vs = 0;
-        uint32_t kp = 0, vp = 0;  // parity of the slot's current use
-        for (int i = 0; i < tiles; ++i) {
-          const int row = k0 + i * kRows;
+        int vs = 0;
+        uint32_t vp = 0;  // parity of the half's current use
+        bool ok = true;
+        for (int i = 0; ok && i < tiles; ++i) {
+          const int row = k0 + i * kRows, ks = i & 1;
           if (i == 0 && half[0]) load_q(0);
-          if (i >= kKeySlots && !mbar_wait_bounded(&k_empty[ks], kp ^ 1u, a.dev_status)) break;
-          mbar_arrive_expect_tx(&k_full[ks], kKeys);
+          if (i >= kKeySlots && !(ok = mbar_wait_bounded(&k_empty[ks], (uint32_t)((i >> 1) & 1) ^ 1u, a.dev_status))) break;
+          mbar_arrive_expect_tx(&k_full[ks], kKeys + (pos ? kAtom : 0u));
           tma_load_3d(smem + lay.k + (uint32_t)ks * kKeys, &p.mk, 0, row, hk * 2, &k_full[ks], keep);
           ++nkl;
-          if (pos) {
-            if (i > 0 && !mbar_wait_bounded(pe_empty, (uint32_t)((i - 1) & 1), a.dev_status)) break;
-            mbar_arrive_expect_tx(pe_full, kAtom);
-            tma_load_2d(smem + lay.pe, &p.mp, 0, row, pe_full, keep);
-            ++npl;
+          if (pos) {  // (its one slot is free when the last tile's keys are)
+            if (i > 0) ok = mbar_wait_bounded(&k_empty[ks ^ 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
+            tma_load_2d(smem + lay.pe, &p.mp, 0, row, &k_full[ks], keep);  // (after a timeout too: it is expected)
+            if (!ok) break;
           }
           if (i == 0 && half[1]) load_q(1);
-          bool ok = true;
-          for (int c = 0; c < 2 && ok; ++c) {
-            if (nvl >= p.nv && !(ok = mbar_wait_bounded(&v_empty[vs], vp ^ 1u, a.dev_status))) break;
-            mbar_arrive_expect_tx(&v_full[vs], kHalf);
-            tma_load_3d(smem + lay.v + (uint32_t)vs * kHalf, &p.mv, 0, row + 64 * c, hk * 2, &v_full[vs], keep);
+          for (int c = 0; c < 2; ++c) {
+            if (nvl >= p.nv && ok) ok = mbar_wait_bounded(&v_empty[vs], vp ^ 1u, a.dev_status);
+            if (!ok && c == 0) break;
+            if (c == 0) mbar_arrive_expect_tx(&v_full[i & 1], 2 * kHalf);
+            tma_load_3d(smem + lay.v + (uint32_t)vs * kHalf, &p.mv, 0, row + 64 * c, hk * 2, &v_full[i & 1], keep);
             ++nvl;
             if (++vs == p.nv) vs = 0, vp ^= 1u;
           }
-          if (!ok) break;
-          if (++ks == kKeySlots) ks = 0, kp ^= 1u;
         }
         // every requested copy lands before the shared memory is released
         if (tiles > 0) {
           for (int w = 0; w < 2; ++w)
-            if (half[w] && (w == 0 || nvl > 0 || !half[0])) mbar_wait_bounded(&q_full[w], 0, nullptr);
-          for (int j = max(0, nkl - kKeySlots); j < nkl; ++j)
-            mbar_wait_bounded(&k_full[j % kKeySlots], (uint32_t)((j / kKeySlots) & 1), nullptr);
-          for (int j = max(0, nvl - p.nv); j < nvl; ++j)
-            mbar_wait_bounded(&v_full[j % p.nv], (uint32_t)((j / p.nv) & 1), nullptr);
-          if (npl > 0) mbar_wait_bounded(pe_full, (uint32_t)((npl - 1) & 1), nullptr);
+            if (half[w]) mbar_wait_bounded(&q_full[w], 0, nullptr);
+          for (int j = max(0, nkl - 2); j < nkl; ++j) mbar_wait_bounded(&k_full[j & 1], (uint32_t)((j >> 1) & 1), nullptr);
+          for (int j = max(0, nvl / 2 - 2); j < nvl / 2; ++j)
+            mbar_wait_bounded(&v_full[j & 1], (uint32_t)((j >> 1) & 1), nullptr);
         }
       }
-    } else if (warp == 1) {
-      // -------------------------------------------------------------- MMA issuer
-      if (tiles > 0 && elect_one()) {
+    } else if (warp == 1 || warp == 3) {
+      // -------------------------------------------------------------- MMA issuers, one a query tile
+      // (one thread for both spent a third of its time testing barriers, which costs hundreds of
+      // cycles while the products read shared memory, and kept the other tile's products waiting)
+      const int w = warp >> 1, n = w ? nt[1] : nt[0];
+      if (n > 0 && elect_one()) {
         const uint32_t id_s = idesc_bf16_f32(128, 128, false, false) | (p.negate ? 1u << 13 : 0u);
         const uint32_t id_o = idesc_bf16_f32(128, 128, false, true);
-        const uint32_t q_addr = smem_u32(smem), k_addr = smem_u32(smem + lay.k), v_addr = smem_u32(smem + lay.v);
-        const uint32_t pe_addr = smem_u32(smem + lay.pe);
+        const uint32_t k_addr = smem_u32(smem + lay.k), v_addr = smem_u32(smem + lay.v);
+        const uint32_t s_col = tmem + (uint32_t)w * 128u, o_col = s_col + kOCol;
+        const uint64_t dq = sw128_desc(smem_u32(smem) + (uint32_t)(w * p.atoms) * kAtom);
+        const uint64_t dp = sw128_desc(smem_u32(smem + lay.pe));
         const int pe_steps = a.dr / 16;
-        bool ok = true;
-        int ks = 0, vs = 0;
-        uint32_t kp = 0, vp = 0;
-        auto issue_s = [&](int w, int st) {
-          const uint64_t dq = sw128_desc(q_addr + (uint32_t)(w * p.atoms) * kAtom);
-          const uint64_t dk = sw128_desc(k_addr + (uint32_t)st * kKeys);
-          const uint32_t d = tmem + (uint32_t)w * 128u;
+        int va = 0;
+        auto issue_s = [&](int i) -> bool {
+          if (!mbar_wait_bounded(&k_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status)) return false;
+          tc_fence_after();
+          const uint64_t dk = sw128_desc(k_addr + (uint32_t)(i & 1) * kKeys);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16(d, dq + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2, dk + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2, id_s,
-                      kk > 0);
-          const uint64_t dqp = dq + 2 * (kAtom >> 4), dp = sw128_desc(pe_addr);
-          for (int kk = 0; kk < pe_steps; ++kk) umma_bf16(d, dqp + 2 * kk, dp + 2 * kk, id_s, 1);
+            umma_bf16(s_col, dq + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2, dk + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2,
+                      id_s, kk > 0);
+          for (int kk = 0; kk < pe_steps; ++kk)
+            umma_bf16(s_col, dq + 2 * (kAtom >> 4) + 2 * kk, dp + 2 * kk, id_s, 1);
           umma_commit(&s_full[w]);
+          umma_commit(&k_empty[i & 1]);
+          return true;
         };
-        // keys of tile i are in
-        auto wait_k = [&](int i) -> bool {
-          return mbar_wait_bounded(&k_full[ks], kp, a.dev_status) &&
-                 (pe_steps == 0 || mbar_wait_bounded(pe_full, (uint32_t)(i & 1), a.dev_status));
-        };
-        // both products with them are issued
-        auto done_k = [&]() {
-          umma_commit(&k_empty[ks]);
-          if (pe_steps > 0) umma_commit(pe_empty);
-          if (++ks == kKeySlots) ks = 0, kp ^= 1u;
-        };
-        ok = wait_k(0);
-        for (int w = 0; w < 2 && ok; ++w)
-          if (nt[w] > 0) {
-            ok = mbar_wait_bounded(&q_full[w], 0, a.dev_status);
-            if (ok) {
-              tc_fence_after();
-              issue_s(w, 0);
-            }
-          }
-        if (ok) done_k();
-        for (int i = 0; ok && i < tiles; ++i) {
-          // (everything that has long arrived is waited for here, not between the products: each
-          // test of a barrier costs some hundred cycles while the products read shared memory)
-          const int va = vs, vb = vs + 1 == p.nv ? 0 : vs + 1;
-          const uint32_t pb = vb == 0 ? vp ^ 1u : vp;
-          const int last_w = i < nt[1] ? 1 : 0;
-          if (!(ok = mbar_wait_bounded(&v_full[va], vp, a.dev_status) && mbar_wait_bounded(&v_full[vb], pb, a.dev_status)))
-            break;
+        bool ok = mbar_wait_bounded(&q_full[w], 0, a.dev_status) && issue_s(0);
+        for (int i = 0; ok && i < n; ++i) {
+          const int vb = va + 1 == p.nv ? 0 : va + 1;
+          if (!(ok = mbar_wait_bounded(&v_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status))) break;
           if (i == tiles - 1 && (i + 1) * kRows > n_k) {  // rows past n_k must not be NaN
             mbar_arrive(partial);
             if (!(ok = mbar_wait_bounded(tail, 0, a.dev_status))) break;
           }
-          if (i + 1 < tiles && !(ok = wait_k(i + 1))) break;
           const uint64_t dva = sw128_mn_desc(v_addr + (uint32_t)va * kHalf, kHalf / 2);
           const uint64_t dvb = sw128_mn_desc(v_addr + (uint32_t)vb * kHalf, kHalf / 2);
-          for (int w = 0; w < 2; ++w) {
-            if (i >= nt[w]) continue;
-            const uint32_t d = tmem + kOCol + (uint32_t)w * 128u, pa = tmem + (uint32_t)w * 128u;
-            if (!(ok = mbar_wait_bounded(&p_half[w], (uint32_t)(i & 1), a.dev_status))) break;
-            tc_fence_after();
+          if (!(ok = mbar_wait_bounded(&p_half[w], (uint32_t)(i & 1), a.dev_status))) break;
+          tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(d, pa + kk * 8, dva + kk * 128, id_o, i > 0 || kk > 0);
-            if (w == last_w) umma_commit(&v_empty[va]);
-            if (!(ok = mbar_wait_bounded(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
-            tc_fence_after();
+          for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(o_col, s_col + kk * 8, dva + kk * 128, id_o, i > 0 || kk > 0);
+          umma_commit(&v_empty[va]);
+          if (!(ok = mbar_wait_bounded(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
+          tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(d, pa + 32 + kk * 8, dvb + kk * 128, id_o, 1);
-            if (i + 1 < nt[w]) issue_s(w, ks);
-            else umma_commit(&o_full[w]);
-          }
-          if (!ok) break;
+          for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(o_col, s_col + 32 + kk * 8, dvb + kk * 128, id_o, 1);
           umma_commit(&v_empty[vb]);
-          if (++vs == p.nv) vs = 0, vp ^= 1u;
-          if (++vs == p.nv) vs = 0, vp ^= 1u;
-          if (i + 1 < tiles) done_k();
+          if (i + 1 < n) ok = issue_s(i + 1);
+          else umma_commit(&o_full[w]);
+          va = vb + 1 == p.nv ? 0 : vb + 1;
         }
         // products left by a timeout get a bounded chance to finish; on the normal path this is
         // the end of the last one
-        umma_commit(drain);
-        mbar_wait_bounded(drain, 0, nullptr);
+        umma_commit(&drain[w]);
+        mbar_wait_bounded(&drain[w], 0, nullptr);
       }
     } else if (warp == 2) {
       // -------------------------------------------------------------- value rows past n_k
@@ -361,9 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
       float t[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        t[c] = __uint_as_float(s[c][0]);
+        t[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-        for (int e = 1; e < 32; ++e) t[c] = fmaxf(t[c], __uint_as_float(s[c][e]));
+        for (int e = 2; e < 32; e += 2) t[c] = max3(t[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
       }
       const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale2, kFloor);
       if (i == 0) {
