@@ -17,9 +17,10 @@
 // and r = 512 it takes 256 TMEM columns, half of the SM's, and the heads are the MMA's N, so
 // few heads cost few cycles.  More than 64 heads are split over CTAs that run side by side and
 // read the tiles through L2.
-//   warp 0: TMA producer; warp 1: MMA issuer; warp 2: zeroes the rows past the length in a
-//   sequence's last tile (they may hold NaN, and 0 * NaN is NaN); warps 4-7: softmax, rescaling
-//   and the output.  S(i + 1) is issued before O(i), so the tensor cores work during softmax(i).
+//   warp 0: TMA producer; warps 1 and 3: MMA issuers of S and of O~; warp 2: zeroes the rows past
+//   the length in a sequence's last tile (they may hold NaN, and 0 * NaN is NaN); warps 4-7:
+//   softmax, rescaling and the output.  S has two buffers, so the tensor cores work on the next
+//   tile during a tile's softmax.
 // The running maximum is a reference that only moves when a score passes it by more than 2^8:
 // the accumulator is then rescaled in TMEM (rare); weights are at most 2^8 and rounded to bf16
 // once, and the sum l adds the rounded weights, so that a weight's rounding cancels where it
@@ -52,9 +53,11 @@ constexpr float kRescale = 8.f;     // log2 units the reference may lag behind
 
 struct Args {
   CUtensorMap mq;     // q [B * Hq][w], box 64 x heads
-  CUtensorMap mc;     // pool rows in blocks of 64 columns, box 64 x tile (x all blocks if w % 64 == 0)
+  CUtensorMap ma, mb; // pool rows in blocks of 64 columns: the blocks of the tile's two pieces (or
+                      // one block at a time in ma, if w % 64 != 0)
   SharedDecodeArgs a;
   int w, na, sa, nm;  // row width, atoms loaded and atoms kept a tile, 128-dim tiles of o~
+  int n0, m0;         // of those, the atoms and 128-dim tiles of the first piece
   int NH, groups, G;  // heads per CTA (a multiple of 16), head groups, CTAs per group
   int nstage;
   int whole_rows;     // w % 64 == 0: one copy brings a tile's atoms
@@ -70,7 +73,7 @@ __host__ __device__ inline Layout layout_of(int na, int sa, int NH, int nstage, 
   l.p = l.stages + (uint32_t)nstage * sa * tile * 128;
   l.ml = l.p + (uint32_t)NH * 128;
   l.bars = l.ml + 3 * kMaxHeads * 4;
-  l.total = l.bars + 8 * (2 * kMaxStages + 12) + 32;
+  l.total = l.bars + 8 * (4 * kMaxStages + 16);
   return l;
 }
 
@@ -101,34 +104,47 @@ __device__ __forceinline__ int valid_length(int L, int most) { return L < 0 || L
 template <int kTok>
 __device__ __forceinline__ int tiles_of(int L) { return (L + kTok - 1) / kTok; }
 
+// Tiles are dealt out by cost: a sequence counts kSegment tiles more than it has, for the query's
+// copy and the output, placed before its first tile.
+constexpr int kSegment = 3;
+
 // The stretch of one sequence's tiles [t0, t1) that a CTA works on.
 struct Segment {
   int b, t0, t1, L;
-  bool first;  // the CTA's first
+  long long at;  // place of tile t0 on the scale by which tiles are dealt out
+  bool first;    // the CTA's first
 };
-// Walks the CTA's tiles sequence by sequence; every warp role walks the same way.
+// Walks the CTA's tiles sequence by sequence; every warp role walks the same way.  `skip`: what is
+// left of the sequence's extra cost, `off`: its next tile, `left`: what is left of the CTA's share,
+// which begins at `at`.
 template <int kTok>
 struct Walk {
   const int32_t* lens;
-  int most, B, b, off, left;
+  int most, B, b, off, skip;
+  long long left, at;
   bool first = true;
   __device__ bool next(Segment& s) {
     while (left > 0 && b < B) {
       const int L = valid_length(__ldg(lens + b), most), n = tiles_of<kTok>(L);
-      if (off >= n) {
-        off = 0;
+      if (n == 0 || skip >= left) {
+        if (n > 0) return false;
         ++b;
         continue;
       }
+      left -= skip;
+      at += skip;
       s.b = b;
       s.L = L;
       s.t0 = off;
-      s.t1 = min(n, off + left);
+      s.t1 = (int)min((long long)n, off + left);
+      s.at = at;
       s.first = first;
       first = false;
       left -= s.t1 - s.t0;
+      at += s.t1 - s.t0;
       ++b;
       off = 0;
+      skip = kSegment;
       return true;
     }
     return false;
@@ -151,43 +167,44 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   float* sm_f = reinterpret_cast<float*>(smem + lay.ml);  // rescale factors
   float* sm_m = sm_f + kMaxHeads;
   float* sm_l = sm_m + kMaxHeads;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars);  // [stages] the tile landed
-  uint64_t* empty = full + kMaxStages;   // [stages] both products have read it
-  uint64_t* q_full = empty + kMaxStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars);  // [stages][2] a piece landed
+  uint64_t* empty = full + 2 * kMaxStages;   // [stages][2] both products have read it
+  uint64_t* q_full = empty + 2 * kMaxStages;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_full + 2;         // [2] S of a tile is in TMEM
-  uint64_t* p_full = q_full + 4;         // P of a tile is in shared memory
-  uint64_t* pv_done = q_full + 5;        // [2] O~ of a tile is added: its P and O~ are free
-  uint64_t* o_free = q_full + 7;         // the segment's O~ has been read
-  uint64_t* drain = q_full + 8;
-  uint64_t* partial = q_full + 9;        // a sequence's last tile is in and is not full
-  uint64_t* tail = q_full + 10;          // its rows past the length are cleared
-  volatile uint32_t* stop = reinterpret_cast<uint32_t*>(q_full + 11);  // the issuer gave up
+  uint64_t* p_full = q_full + 4;         // [2] P of a tile is in shared memory, its S has been read
+  uint64_t* pv_done = q_full + 6;        // [2] O~ of a tile is added: its P and O~ are free
+  uint64_t* o_free = q_full + 8;         // the segment's O~ has been read
+  uint64_t* drain = q_full + 9;          // [2]
+  uint64_t* partial = q_full + 11;       // a sequence's last tile is in and is not full
+  uint64_t* tail = q_full + 12;          // its rows past the length are cleared
+  volatile uint32_t* stop = reinterpret_cast<uint32_t*>(q_full + 13);  // the first issuer gave up
 
   if ((smem_u32(smem) & 1023u) != 0) {  // swizzled operands need 1 KiB alignment
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < kMaxStages; ++i) {
+    for (int i = 0; i < 2 * kMaxStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kSoftWarps);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&drain[i], 1);
+    }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
-    mbar_init(p_full, kSoftWarps);
-    mbar_init(&pv_done[0], 1);
-    mbar_init(&pv_done[1], 1);
     mbar_init(o_free, kSoftWarps);
-    mbar_init(drain, 1);
     mbar_init(partial, 1);
     mbar_init(tail, 1);
     *stop = 0;
     fence_barrier_init();
     prefetch_tensormap(&p.mq);
-    prefetch_tensormap(&p.mc);
+    prefetch_tensormap(&p.ma);
+    prefetch_tensormap(&p.mb);
   }
   if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
 
@@ -195,11 +212,15 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   pdl_launch_dependents();
   // where this CTA's tiles begin: a prefix sum of the sequences' tile counts
   const int per_thread = (a.B + kThreads - 1) / kThreads, c0 = tid * per_thread, c1 = min(a.B, c0 + per_thread);
+  auto cost_of = [&](int b) {
+    const int n = tiles_of<kTok>(valid_length(__ldg(a.seq_lens + b), a.max_seq_len));
+    return n > 0 ? n + kSegment : 0;
+  };
   int sum = 0;
   for (int b = c0; b < c1; ++b) {
     const int L = __ldg(a.seq_lens + b);
     if (valid_length(L, a.max_seq_len) != L && blockIdx.x == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
-    sum += tiles_of<kTok>(valid_length(L, a.max_seq_len));
+    sum += cost_of(b);
   }
   int incl = sum;
 #pragma unroll
@@ -223,34 +244,34 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   if (count > 0 && g0 >= incl - sum && g0 < incl) {  // one thread's sequences hold the first tile
     int at = incl - sum, b = c0;
     for (;; ++b) {
-      const int n = tiles_of<kTok>(valid_length(__ldg(a.seq_lens + b), a.max_seq_len));
+      const int n = cost_of(b);
       if (g0 < at + n) break;
       at += n;
     }
     start_b = b;
-    start_off = (int)(g0 - at);
+    start_off = (int)(g0 - at) - kSegment;  // negative: cost before the first tile
   }
   __syncthreads();
   const uint32_t tmem = tmem_slot;
-  Walk<kTok> walk{a.seq_lens, a.max_seq_len, a.B, count > 0 ? start_b : 0, count > 0 ? start_off : 0, count};
+  Walk<kTok> walk{a.seq_lens, a.max_seq_len, a.B, count > 0 ? start_b : 0, count > 0 ? max(0, start_off) : 0,
+                  count > 0 ? max(0, -start_off) : 0, count, g0};
   Segment seg;
 
+  const int pieces = p.n0 < p.na ? 2 : 1;
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    if (count > 0) {
+    if (count > 0 && elect_one()) {
+      int got[2] = {0, 0};  // tiles of which the piece is requested
       const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
       int i = 0, segs = 0;
       Ring ring{p.nstage};
       bool ok = true;
       while (ok && walk.next(seg)) {
-        if (segs > 0) ok = __all_sync(~0u, mbar_wait_bounded(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status));
+        if (segs > 0) ok = mbar_wait_bounded(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status);
         if (!ok) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128));
-          for (int c = 0; c < p.na; ++c)
-            tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, seg.b * a.Hq + h_base, q_full, keep);
-        }
-        __syncwarp();
+        mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128));
+        for (int c = 0; c < p.na; ++c)
+          tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, seg.b * a.Hq + h_base, q_full, keep);
         ++segs;
         const int32_t* entry = a.block_table + (size_t)seg.b * a.max_pages + seg.t0 * kTok / a.page_size;
         int in_page = seg.t0 * kTok % a.page_size, page = __ldg(entry);
@@ -264,87 +285,107 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
                                                           : a.num_pages * a.page_size;
           in_page += kTok;
           const int st = ring.st;
-          if (i >= p.nstage && !(ok = __all_sync(~0u, mbar_wait_bounded(&empty[st], ring.ph ^ 1u, a.dev_status))))
-            break;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&full[st], (uint32_t)(p.na * kAtom));
-            uint8_t* dst = smem + lay.stages + (uint32_t)(st * p.sa) * kAtom;
+          uint8_t* dst = smem + lay.stages + (uint32_t)(st * p.sa) * kAtom;
+          for (int piece = 0; piece < pieces; ++piece) {
+            uint64_t* bar = &full[2 * st + piece];
+            if (i >= p.nstage && !(ok = mbar_wait_bounded(&empty[2 * st + piece], ring.ph ^ 1u, a.dev_status))) break;
+            const int c0 = piece ? p.n0 : 0, c1 = piece ? p.na : p.n0;
+            mbar_arrive_expect_tx(bar, (uint32_t)((c1 - c0) * kAtom));
             if (p.whole_rows) {
-              tma_load_3d(dst, &p.mc, 0, row, 0, &full[st], once);
+              tma_load_3d(dst + c0 * kAtom, piece ? &p.mb : &p.ma, 0, row, c0, bar, once);
             } else {
-              for (int c = 0; c < p.na; ++c) tma_load_2d(dst + c * kAtom, &p.mc, 64 * c, row, &full[st], once);
+              for (int c = c0; c < c1; ++c) tma_load_2d(dst + c * kAtom, &p.ma, 64 * c, row, bar, once);
             }
+            got[piece] = i + 1;
           }
-          __syncwarp();
+          if (!ok) break;
         }
       }
       // every requested copy lands before the shared memory is released (bounded; on the normal
       // path nothing is outstanding: the MMA warp has waited for each)
       if (segs > 0) mbar_wait_bounded(q_full, (uint32_t)((segs - 1) & 1), nullptr);
-      for (int k = max(0, i - p.nstage); k < i; ++k)
-        mbar_wait_bounded(&full[k % p.nstage], (uint32_t)((k / p.nstage) & 1), nullptr);
+      for (int piece = 0; piece < pieces; ++piece)
+        for (int k = max(0, got[piece] - p.nstage); k < got[piece]; ++k)
+          mbar_wait_bounded(&full[2 * (k % p.nstage) + piece], (uint32_t)((k / p.nstage) & 1), nullptr);
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    const uint32_t id_s = idesc_bf16_f32(64, kTok, false, false);
-    const uint32_t id_o = idesc_bf16_f32(128, p.NH, true, false);
-    const uint32_t q_addr = smem_u32(smem), p_addr = smem_u32(smem + lay.p);
-    bool ok = true;
-    int i = 0, segs = 0;
-    Ring rs{p.nstage}, ro{p.nstage};  // the next tile to score, the next to add up
-    const uint32_t stage0 = smem_u32(smem + lay.stages), stage_bytes = (uint32_t)p.sa * kAtom;
-    const uint32_t q_step = (uint32_t)(p.NH * 128) >> 4;
-    const int steps_left = p.w % 64 / 16;
-    // One thread runs the whole loop: under the products' shared-memory traffic every barrier
-    // test, shuffle or vote between them costs 100 cycles and more.
+    // ---------------------------------------------------------------- S issuer
+    // (One thread runs the whole loop: under the products' shared-memory traffic every barrier
+    // test, shuffle or vote between them costs 100 cycles and more.  The two products have a
+    // thread each, so that neither waits for what the other one lacks.)
     if (elect_one()) {
-      int tails = 0;
-      // S of tile k (tile t of the segment) once its rows are in
-      auto issue_s = [&](int k, int t, bool landed) -> bool {
-        if (!landed && !mbar_wait_bounded(&full[rs.st], rs.ph, a.dev_status)) return false;
-        if ((t + 1) * kTok > seg.L) {  // what lies past the length has been cleared
-          mbar_arrive(partial);
-          if (!mbar_wait_bounded(tail, (uint32_t)(tails & 1), a.dev_status)) return false;
-          ++tails;
-        }
-        tc_fence_after();
-        // (descriptors advance by additions, four steps at a time: building each one took longer
-        // than its product)
-        const uint32_t d = tmem + kSCol + (uint32_t)(k & 1) * kTok;
-        uint64_t dq = sw128_desc(q_addr), dt = sw128_desc(stage0 + (uint32_t)rs.st * stage_bytes);
-        uint32_t acc = 0;
-        for (int c = 0; c < p.w / 64; ++c) {
-          umma_bf16(d, dq, dt, id_s, acc);
-          umma_bf16(d, dq + 2, dt + 2, id_s, 1);
-          umma_bf16(d, dq + 4, dt + 4, id_s, 1);
-          umma_bf16(d, dq + 6, dt + 6, id_s, 1);
-          dq += q_step;
-          dt += kAtom >> 4;
-          acc = 1;
-        }
-        for (int kk = 0; kk < steps_left; ++kk) {
-          umma_bf16(d, dq + 2 * kk, dt + 2 * kk, id_s, acc);
-          acc = 1;
-        }
-        umma_commit(&s_full[k & 1]);
-        if (t == seg.t1 - 1) umma_commit(q_empty);  // the segment's last product with its q~
-        rs.next();
-        return true;
-      };
+      const uint32_t id_s = idesc_bf16_f32(64, kTok, false, false);
+      const uint32_t stage0 = smem_u32(smem + lay.stages), stage_bytes = (uint32_t)p.sa * kAtom;
+      const uint32_t q_step = (uint32_t)(p.NH * 128) >> 4;
+      const int whole0 = min(p.n0, p.w / 64), whole1 = p.w / 64 - whole0, steps_left = p.w % 64 / 16;
+      Ring ring{p.nstage};
+      bool ok = true;
+      int i = 0, segs = 0, tails = 0;
       while (ok && walk.next(seg)) {
-        ok = mbar_wait_bounded(q_full, (uint32_t)(segs & 1), a.dev_status) && issue_s(i, seg.t0, false);
-        bool ahead = true;  // S of tile i is issued
-        for (int t = seg.t0; ok && t < seg.t1; ++t, ++i) {
-          if (!ahead && !(ok = issue_s(i, t, false))) break;
-          // the next tile's S goes first if its rows are in; otherwise this tile's product does
-          ahead = t + 1 < seg.t1 && mbar_test(&full[rs.st], rs.ph);
-          if (ahead && !(ok = issue_s(i + 1, t + 1, true))) break;
-          if (t == seg.t0 && segs > 0 &&
-              !(ok = mbar_wait_bounded(o_free, (uint32_t)((segs - 1) & 1), a.dev_status)))
-            break;
-          if (!(ok = mbar_wait_bounded(p_full, (uint32_t)(i & 1), a.dev_status))) break;
+        ok = mbar_wait_bounded(q_full, (uint32_t)(segs & 1), a.dev_status);
+        for (int t = seg.t0; ok && t < seg.t1; ++t, ++i, ring.next()) {
+          const bool last = (t + 1) * kTok > seg.L;  // not full: what lies past the length is cleared first
+          if (i >= 2 && !(ok = mbar_wait_bounded(&p_full[i & 1], (uint32_t)((i >> 1) & 1) ^ 1u, a.dev_status))) break;
+          if (!(ok = mbar_wait_bounded(&full[2 * ring.st], ring.ph, a.dev_status))) break;
+          if (last) {
+            if (pieces > 1 && !(ok = mbar_wait_bounded(&full[2 * ring.st + 1], ring.ph, a.dev_status))) break;
+            mbar_arrive(partial);
+            if (!(ok = mbar_wait_bounded(tail, (uint32_t)(tails & 1), a.dev_status))) break;
+            ++tails;
+          }
           tc_fence_after();
-          uint64_t dt = sw128_mn_desc(stage0 + (uint32_t)ro.st * stage_bytes, kAtom);
+          // (descriptors advance by additions, four steps at a time: building each one took longer
+          // than its product)
+          const uint32_t d = tmem + kSCol + (uint32_t)(i & 1) * kTok;
+          uint64_t dq = sw128_desc(smem_u32(smem)), dt = sw128_desc(stage0 + (uint32_t)ring.st * stage_bytes);
+          uint32_t acc = 0;
+          auto blocks = [&](int n) {
+            for (int c = 0; c < n; ++c) {
+              umma_bf16(d, dq, dt, id_s, acc);
+              umma_bf16(d, dq + 2, dt + 2, id_s, 1);
+              umma_bf16(d, dq + 4, dt + 4, id_s, 1);
+              umma_bf16(d, dq + 6, dt + 6, id_s, 1);
+              dq += q_step;
+              dt += kAtom >> 4;
+              acc = 1;
+            }
+          };
+          blocks(whole0);
+          if (pieces > 1) {
+            if (!last && !(ok = mbar_wait_bounded(&full[2 * ring.st + 1], ring.ph, a.dev_status))) break;
+            tc_fence_after();
+            blocks(whole1);
+          }
+          for (int kk = 0; kk < steps_left; ++kk) {
+            umma_bf16(d, dq + 2 * kk, dt + 2 * kk, id_s, acc);
+            acc = 1;
+          }
+          umma_commit(&s_full[i & 1]);
+          if (t == seg.t1 - 1) umma_commit(q_empty);  // the segment's last product with its q~
+        }
+        ++segs;
+      }
+      if (!ok) *stop = 1;
+      // products left by a timeout get a bounded chance to finish; on the normal path this is the
+      // end of the last one
+      umma_commit(&drain[0]);
+      mbar_wait_bounded(&drain[0], 0u, nullptr);
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- O~ issuer
+    if (elect_one()) {
+      const uint32_t id_o = idesc_bf16_f32(128, p.NH, true, false);
+      const uint32_t stage0 = smem_u32(smem + lay.stages), stage_bytes = (uint32_t)p.sa * kAtom;
+      const uint32_t p_addr = smem_u32(smem + lay.p);
+      Ring ring{p.nstage};
+      bool ok = true;
+      int i = 0, segs = 0;
+      while (ok && walk.next(seg)) {
+        if (segs > 0) ok = mbar_wait_bounded(o_free, (uint32_t)((segs - 1) & 1), a.dev_status);
+        for (int t = seg.t0; ok && t < seg.t1; ++t, ++i, ring.next()) {
+          if (!(ok = mbar_wait_bounded(&p_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status))) break;
+          tc_fence_after();
+          uint64_t dt = sw128_mn_desc(stage0 + (uint32_t)ring.st * stage_bytes, kAtom);
           const uint64_t dp = sw128_desc(p_addr + (kTok == 32 ? (uint32_t)(i & 1) * 64u : 0u));
           for (int m = 0; m < p.nm; ++m, dt += 2 * kAtom >> 4) {
             const uint32_t d = tmem + (uint32_t)(m * p.NH);
@@ -354,19 +395,15 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
               umma_bf16(d, dt + 256, dp + 4, id_o, 1);
               umma_bf16(d, dt + 384, dp + 6, id_o, 1);
             }
+            if (m == p.m0 - 1) umma_commit(&empty[2 * ring.st]);
           }
-          umma_commit(&empty[ro.st]);
+          if (pieces > 1) umma_commit(&empty[2 * ring.st + 1]);
           umma_commit(&pv_done[i & 1]);
-          ro.next();
         }
         ++segs;
       }
-      if (!ok) {
-        *stop = 1;
-        // products left by a timeout get a bounded chance to finish
-        umma_commit(drain);
-        mbar_wait_bounded(drain, 0u, nullptr);
-      }
+      umma_commit(&drain[1]);
+      mbar_wait_bounded(&drain[1], 0u, nullptr);
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- rows past the length
@@ -492,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && !bad) mbar_arrive(p_full);
+        if (lane == 0 && !bad) mbar_arrive(&p_full[i & 1]);
       }
       // the segment's sums; O~ is complete with its last tile's product
       l0 += __shfl_xor_sync(~0u, l0, 1);
@@ -545,9 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       if (!whole && th < nheads) ml[th] = make_float2(sm_m[th], sm_l[th]);
       // the CTAs that hold this sequence, for the merge: written by the one with its first tile
       if (seg.t0 == 0 && th == 0 && group == 0) {
-        const long long first = g0 + i - (seg.t1 - seg.t0);
         reinterpret_cast<int2*>(ws)[seg.b] =
-            make_int2(cta * 2 + (seg.first ? 0 : 1), whole ? -1 : (int)((first + n - 1) / per));
+            make_int2(cta * 2 + (seg.first ? 0 : 1), whole ? -1 : (int)((seg.at + n - 1) / per));
       }
       named_bar_sync(1, 128);  // sm_l, sm_m and O~ have been read
       if (lane == 0) mbar_arrive(o_free);
@@ -563,71 +599,106 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
 }
 
 // Joins the partial states of sequences that several CTAs hold, and writes the zeros of empty
-// ones.  An item is 128 dims of one head: one warp (kWarps = 1), or a whole CTA whose warps
-// share the partial states (few sequences, many parts each).
+// ones.  A warp takes 512 dims of a head (kWarps = 1), or, where few sequences have many parts
+// each, a CTA takes 128 dims of a head and its warps share the parts.  Bound by latency: the
+// lengths and the meta word are read together, then everything else of up to kBatch parts.
 template <int kWarps>
 __global__ void __launch_bounds__(256) stief_shared_merge_kernel(const SharedDecodeArgs a, int NH, int groups, int G) {
+  constexpr int kVec = kWarps == 1 ? 4 : 1;     // 128-dim chunks a warp holds
+  constexpr int kBatch = kWarps == 1 ? 2 : 8;   // parts in flight
   __shared__ float4 acc_s[8][32];
-  __shared__ float red_s[8][2];
+  __shared__ float2 ml_s[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
   const int nd = (a.r + 127) / 128;
-  const int item = kWarps == 1 ? (int)blockIdx.x * 8 + warp : (int)blockIdx.x;
-  const int h = item / nd, d = (item % nd) * 128 + lane * 4;
+  const int h = kWarps == 1 ? (int)blockIdx.x * 8 + warp : (int)blockIdx.x / nd;
+  const int d0 = (kWarps == 1 ? 0 : (int)blockIdx.x % nd * 128) + lane * 4;
+  uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
   pdl_wait();
   pdl_launch_dependents();
   const int L = valid_length(__ldg(a.seq_lens + b), a.max_seq_len);
-  uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
-  const int2 meta = L > 0 ? *reinterpret_cast<const int2*>(ws + (size_t)b * 8) : make_int2(0, 0);
+  const int2 meta = __ldcg(reinterpret_cast<const int2*>(ws + (size_t)b * 8));  // (garbage if L == 0)
   if (L > 0 && meta.y < 0) return;  // whole: written already
   if (h >= a.Hq) return;            // (kWarps == 8: never, the grid is exact)
-  uint16_t* out = a.out + ((size_t)b * a.Hq + h) * a.r + d;
+  uint16_t* out = a.out + ((size_t)b * a.Hq + h) * a.r + d0;
   if (L == 0) {
-    if (d < a.r && (kWarps == 1 || warp == 0)) *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
+    if (kWarps == 1 || warp == 0)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (d0 + 128 * j < a.r) *reinterpret_cast<uint2*>(out + 128 * j) = make_uint2(0, 0);
     return;
   }
-  // partial state k is in CTA c = meta.x / 2 + k of the head's group: slot 0 but for the first
+  // part k is in CTA c = meta.x / 2 + k of the head's group: slot 0 but for the first
   const int group = h / NH, hl = h % NH, c_first = meta.x >> 1, n = meta.y - c_first + 1;
   if (c_first < 0 || n < 1 || meta.y >= G) return;  // the first kernel gave up on a wait
   const float2* ml = reinterpret_cast<const float2*>(ws + meta_bytes(a.B));
   const float* part = reinterpret_cast<const float*>(ws + meta_bytes(a.B) + ml_bytes());
-  auto slot_of = [&](int k) { return ((c_first + k) * groups + group) * 2 + (k == 0 ? (meta.x & 1) : 0); };
-  float M = -INFINITY;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, ml[(size_t)slot_of(k) * kMaxHeads + hl].x);
+  float M = -INFINITY, l = 0.f;
+  float4 acc[kVec];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  const int w0 = kWarps == 1 ? 0 : warp;
-#pragma unroll 4
-  for (int k = w0; k < n; k += kWarps) {
-    const size_t s = (size_t)slot_of(k);
-    const float2 e = ml[s * kMaxHeads + hl];
-    const float4 o = d < a.r ? *reinterpret_cast<const float4*>(part + (s * NH + hl) * a.r + d)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float f = fast_exp2(e.x - M);
-    l += f * e.y;
-    acc.x += f * o.x;
-    acc.y += f * o.y;
-    acc.z += f * o.z;
-    acc.w += f * o.w;
-  }
-  if (kWarps > 1) {
-    acc_s[warp][lane] = acc;
-    if (lane == 0) red_s[warp][0] = l;
-    __syncthreads();
-    if (warp != 0) return;
-    for (int k = 1; k < 8; ++k) {
-      const float4 o = acc_s[k][lane];
-      acc.x += o.x;
-      acc.y += o.y;
-      acc.z += o.z;
-      acc.w += o.w;
-      l += red_s[k][0];
+  for (int j = 0; j < kVec; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = kWarps == 1 ? 0 : warp; k0 < n; k0 += kWarps * kBatch) {
+    float2 e[kBatch];
+    float4 o[kBatch][kVec];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = k0 + kWarps * i;
+      e[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) o[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < n) {
+        const size_t s = (size_t)(((c_first + k) * groups + group) * 2 + (k == 0 ? (meta.x & 1) : 0));
+        e[i] = __ldcg(ml + s * kMaxHeads + hl);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          if (d0 + 128 * j < a.r)
+            o[i][j] = __ldcg(reinterpret_cast<const float4*>(part + (s * NH + hl) * a.r + d0 + 128 * j));
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, e[i].x);
+    const float f0 = fast_exp2(M - top);  // (M is finite after the first batch; 2^-inf = 0 before)
+    M = top;
+    l *= f0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) acc[j].x *= f0, acc[j].y *= f0, acc[j].z *= f0, acc[j].w *= f0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float f = fast_exp2(e[i].x - M);
+      l += f * e[i].y;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        acc[j].x += f * o[i][j].x;
+        acc[j].y += f * o[i][j].y;
+        acc[j].z += f * o[i][j].z;
+        acc[j].w += f * o[i][j].w;
+      }
     }
   }
-  if (d < a.r)
-    *reinterpret_cast<uint2*>(out) =
-        make_uint2(pack_bf16x2_rn(acc.x / l, acc.y / l), pack_bf16x2_rn(acc.z / l, acc.w / l));
+  if (kWarps > 1) {
+    acc_s[warp][lane] = acc[0];
+    if (lane == 0) ml_s[warp] = make_float2(M, l);
+    __syncthreads();
+    if (warp != 0) return;
+    for (int k = 1; k < 8; ++k) M = fmaxf(M, ml_s[k].x);
+    l = 0.f;
+    acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < 8; ++k) {
+      const float f = fast_exp2(ml_s[k].x - M);
+      const float4 o = acc_s[k][lane];
+      l += f * ml_s[k].y;
+      acc[0].x += f * o.x;
+      acc[0].y += f * o.y;
+      acc[0].z += f * o.z;
+      acc[0].w += f * o.w;
+    }
+  }
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int j = 0; j < kVec; ++j)
+    if (d0 + 128 * j < a.r)
+      *reinterpret_cast<uint2*>(out + 128 * j) = make_uint2(pack_bf16x2_rn(acc[j].x * inv, acc[j].y * inv),
+                                                            pack_bf16x2_rn(acc[j].z * inv, acc[j].w * inv));
 }
 
 size_t shared_decode_workspace_bytes(int B, int Hq, int r) {
@@ -658,11 +729,22 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   if (!encode_tiled_bf16_2d(&p.mq, a.q, (uint64_t)p.w, (uint64_t)a.B * a.Hq, pitch, 64, (uint32_t)p.NH,
                             CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  if (!(p.whole_rows ? encode_tiled_bf16_3d(&p.mc, a.pages, {64, rows, (uint64_t)p.na}, {pitch, 128},
-                                            {64, (uint32_t)tile, (uint32_t)p.na})
-                     : encode_tiled_bf16_2d(&p.mc, a.pages, (uint64_t)p.w, rows, pitch, 64, (uint32_t)tile,
-                                            CU_TENSOR_MAP_SWIZZLE_128B)))
-    return cudaErrorInvalidValue;
+  // The tile comes in two pieces, split between 128-dim tiles of o~: the first half's memory is
+  // free again, and its next rows under way, while the second half's product runs.
+  p.m0 = (p.nm + 1) / 2;
+  p.n0 = p.na < 2 * p.m0 ? p.na : 2 * p.m0;
+  const uint32_t n1 = (uint32_t)(p.na - p.n0);
+  if (p.whole_rows) {
+    if (!encode_tiled_bf16_3d(&p.ma, a.pages, {64, rows, (uint64_t)p.na}, {pitch, 128},
+                              {64, (uint32_t)tile, (uint32_t)p.n0}) ||
+        !encode_tiled_bf16_3d(&p.mb, a.pages, {64, rows, (uint64_t)p.na}, {pitch, 128},
+                              {64, (uint32_t)tile, n1 > 0 ? n1 : 1u}))
+      return cudaErrorInvalidValue;
+  } else {
+    if (!encode_tiled_bf16_2d(&p.ma, a.pages, (uint64_t)p.w, rows, pitch, 64, (uint32_t)tile, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+    p.mb = p.ma;
+  }
   const auto kern = stief_shared_decode_kernel<kTile>;
   static SmemLimit limit;
   cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kern), a.device, (int)smem);
@@ -679,15 +761,14 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return e;
-  const int items = a.Hq * p.nm;
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  // many parts a sequence: a CTA an item, its warps share the parts; else a warp an item
+  // many parts a sequence: a CTA's warps share them; else a warp a head
   if (p.G > 8 * a.B) {
-    cfg.gridDim = dim3(items, a.B);
+    cfg.gridDim = dim3(a.Hq * p.nm, a.B);
     return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<8>, a, p.NH, p.groups, p.G);
   }
-  cfg.gridDim = dim3((items + 7) / 8, a.B);
+  cfg.gridDim = dim3((a.Hq + 7) / 8, a.B);
   return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<1>, a, p.NH, p.groups, p.G);
 }
 
