@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
             tmem_ld16(tmem + lane_addr + (uint32_t)c, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * sm_f[c % p.NH + e]);
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * lds_f32(smem_u32(sm_f + c % p.NH + e)));
             tmem_st16(tmem + lane_addr + (uint32_t)c, v);
           }
           tmem_wait_st();
@@ -565,10 +565,22 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
           tmem_wait_ld();
           const int nh = d < a.r ? nheads - c : 0;  // heads to store
           if (whole) {
-            uint16_t* o = a.out + ((size_t)seg.b * a.Hq + h_base + c) * a.r + d;
+            // (all factors first: read between the stores, each load would wait for the last store)
+            float4 f[8];
 #pragma unroll
-            for (int e = 0; e < 32; ++e, o += a.r)
-              if (e < nh) *o = f32_to_bf16_rn(__uint_as_float(v[e >> 4][e & 15]) * sm_f[c + e]);
+            for (int e = 0; e < 8; ++e) f[e] = lds128f(smem_u32(sm_f + c + 4 * e));
+            // neighbouring lanes swap halves of each pair of heads: an even lane stores its dim and
+            // the next of the first head, an odd one its dim and the one before of the second
+            const int odd = lane & 1;
+            uint16_t* o = a.out + ((size_t)seg.b * a.Hq + h_base + c + odd) * a.r + d - odd;
+#pragma unroll
+            for (int e = 0; e < 32; e += 2, o += 2 * (size_t)a.r) {
+              const float4 g = f[e >> 2];
+              const float x0 = __uint_as_float(v[e >> 4][e & 15]) * ((e & 2) ? g.z : g.x);
+              const float x1 = __uint_as_float(v[e >> 4][(e + 1) & 15]) * ((e & 2) ? g.w : g.y);
+              const float y = __shfl_xor_sync(~0u, odd ? x0 : x1, 1);
+              if (e + odd < nh) *reinterpret_cast<uint32_t*>(o) = odd ? pack_bf16x2_rn(y, x1) : pack_bf16x2_rn(x0, y);
+            }
           } else {
             float* o = part + (size_t)c * a.r + d;
 #pragma unroll
