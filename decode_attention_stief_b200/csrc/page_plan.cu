@@ -4,7 +4,7 @@
 // For sequence b with L_b cached tokens and T_b new ones (page size s, capacity C tokens):
 //     q_start[b] = sum_{a<b} max(T_a, 0)
 //     need_b = ceil((L_b + T_b) / s) - ceil(L_b / s)        new pages
-//     P_b    = sum_{a<=b} need_a                            (refused ones below count 0)
+//     P_b    = sum_{a<=b} need_a
 // Page j < need_b of b is free_pages[n - 1 - (P_b - need_b + j)], n = *free_count: the top of
 // the free stack first, in sequence order.  Token i of b is slot page(t / s) * s + t % s with
 // t = L_b + i.  Three prefix sums over B (tokens, pages, lengths) decide everything; each
@@ -24,7 +24,7 @@ namespace stief {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanTokensPerCta = 8192;  // slots a CTA writes (two per thread and store round)
+constexpr int kSmallThreads = 256;
 
 // Inclusive prefix sum over the CTA (64-bit), and its total.
 __device__ long long block_scan(long long v, long long* warp_sums, long long* total) {
@@ -137,8 +137,9 @@ __global__ void __launch_bounds__(kPlanThreads) stief_page_plan_kernel(const Pla
     sum += have[b] >= 0 ? (long long)L + a.new_tokens[b] : (L < 0 || L > cap) ? 0 : L;
   }
   if (used > 0) atomicMax(&used_s, used);
-  long long kv = block_scan(sum, warp_sums, &total) - sum;
+  __syncthreads();
   if (blockIdx.x == 0) {
+    long long kv = block_scan(sum, warp_sums, &total) - sum;
     if (bits) report(a.dev_status, bits);
     for (int b = b0; b < b1; ++b) {
       const int L = a.seq_lens[b];
@@ -179,24 +180,53 @@ __global__ void __launch_bounds__(kPlanThreads) stief_page_plan_kernel(const Pla
 
   // slots: the CTA's share of the flat tokens
   if (!a.slots) return;
-  const int chunk = (a.max_tokens + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int i1 = min(a.max_tokens, ((int)blockIdx.x + 1) * chunk);
-  for (int i = (int)blockIdx.x * chunk + tid; i < i1; i += nthreads) {
-    int slot = -1;
-    if (i < total_tokens) {
-      const int b = upper_index(qs, B, i);
-      if (have[b] >= 0) {
-        const int t = have[b] + (i - qs[b]), pi = t / ps;
-        const int page = pi < first[b] ? tail[b] : a.free_pages[n - 1 - (upto[b] + pi - first[b])];
-        if (page >= 0 && page < a.num_pages) slot = page * ps + t % ps;
+  // (one bisection and one division for four tokens; 16-byte stores if the array allows them)
+  const bool wide = (reinterpret_cast<uintptr_t>(a.slots) & 15u) == 0;
+  for (long long i0 = 4LL * ((long long)blockIdx.x * nthreads + tid); i0 < a.max_tokens;
+       i0 += 4LL * nthreads * gridDim.x) {
+    int s[4] = {-1, -1, -1, -1};
+    if (i0 < total_tokens) {
+      int b = upper_index(qs, B, (int)i0), page = -1, at = ps;  // at: offset in the page, ps: look up
+      int next = b + 1 < B ? qs[b + 1] : sat32(total_tokens), pi = 0;
+      bool fresh = true;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = (int)i0 + e;
+        if (i >= total_tokens || i >= a.max_tokens) break;
+        while (i >= next) {  // (sequences without new tokens are passed over)
+          ++b;
+          next = b + 1 < B ? qs[b + 1] : sat32(total_tokens);
+          fresh = true;
+        }
+        if (have[b] < 0) continue;
+        if (fresh) {
+          const int t = have[b] + (i - qs[b]);
+          pi = t / ps;
+          at = t - pi * ps;
+        } else if (++at == ps) {
+          at = 0;
+          ++pi;
+          fresh = true;
+        }
+        if (fresh) page = pi < first[b] ? tail[b] : a.free_pages[n - 1 - (upto[b] + pi - first[b])];
+        fresh = false;
+        s[e] = page >= 0 && page < a.num_pages ? page * ps + at : -1;
       }
     }
-    a.slots[i] = slot;
+    if (wide && i0 + 4 <= a.max_tokens) {
+      *reinterpret_cast<int4*>(a.slots + i0) = make_int4(s[0], s[1], s[2], s[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i0 + e < a.max_tokens) a.slots[i0 + e] = s[e];
+    }
   }
 }
 
 cudaError_t launch_page_plan(const PlanArgs& a, int sms, cudaStream_t stream) {
-  int grid = a.slots ? (a.max_tokens + kPlanTokensPerCta - 1) / kPlanTokensPerCta : 1;
+  // a step of few sequences and tokens has little to scan: fewer warps meet sooner
+  const int threads = a.B <= kSmallThreads && a.max_tokens <= 4 * kSmallThreads ? kSmallThreads : kPlanThreads;
+  long long grid = a.slots ? (a.max_tokens + 4LL * threads - 1) / (4 * threads) : 1;
   if (grid < 1) grid = 1;
   if (grid > sms) grid = sms;
   const int smem = 6 * 4 * a.B;
@@ -204,8 +234,8 @@ cudaError_t launch_page_plan(const PlanArgs& a, int sms, cudaStream_t stream) {
   cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_page_plan_kernel), a.device, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

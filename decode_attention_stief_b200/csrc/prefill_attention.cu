@@ -33,12 +33,8 @@ namespace {
 
 constexpr int kRows = 128;                 // queries a tile, keys a tile
 constexpr uint32_t kAtom = kRows * 128;    // bytes of 128 rows x 64 columns
-constexpr int kThreads = 384;
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kOCol = 256;            // S_w at 128 w, O_w at 256 + 128 w
 constexpr float kRescale = 8.f;
 constexpr float kFloor = -1e30f;
-constexpr int kKeySlots = 2;
 constexpr int kMaxHalves = 4;  // (no more: a tile's barrier, one of two in turn, is armed again only
                                // after a wait for the halves of two tiles before)
 constexpr uint32_t kKeys = 2 * kAtom;      // bytes of a key tile without the position part
@@ -57,19 +53,20 @@ struct Args {
   int negate;       // scale < 0: the products are negated instead
 };
 
-// Queries (two tiles), key slots, one slot of position parts, slots of 64 value rows.  A key tile's
+// Queries (kW tiles), key slots, one slot of position parts, slots of 64 value rows.  A key tile's
 // position part is wanted between its two products only, so one slot of it is enough, and what
 // that saves holds a third half tile of values: with two, the next one arrived too late.
 struct Layout {
   uint32_t k, pe, v, bars, total;
 };
+template <int kW>
 __host__ __device__ inline Layout layout_of(int atoms, int nv) {
   Layout l;
-  l.k = 2u * atoms * kAtom;
-  l.pe = l.k + kKeySlots * kKeys;
+  l.k = (uint32_t)(kW * atoms) * kAtom;
+  l.pe = l.k + kW * kKeys;  // (as many key slots as tiles of queries)
   l.v = l.pe + (uint32_t)(atoms - 2) * kAtom;
   l.bars = l.v + (uint32_t)nv * kHalf;
-  l.total = l.bars + 8 * (2 * kKeySlots + 2 + kMaxHalves + 16);
+  l.total = l.bars + 8 * (4 + 2 + kMaxHalves + 16);
   return l;
 }
 
@@ -96,12 +93,17 @@ __device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uin
 
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid_constant__ Args p) {
+template <int kW>
+__global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
+    stief_prefill_kernel(const __grid_constant__ Args p) {
+  constexpr uint32_t kTmemCols = kW * 256;   // S_w at 128 w, O_w at 128 (kW + w)
+  constexpr uint32_t kOCol = kW * 128;
+  constexpr int kKeySlots = kW;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t tmem_slot;
   const PrefillArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Layout lay = layout_of(p.atoms, p.nv);
+  const Layout lay = layout_of<kW>(p.atoms, p.nv);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + lay.bars);
   uint64_t* k_empty = k_full + kKeySlots;
   uint64_t* v_full = k_empty + kKeySlots;   // [2] both halves of a value tile, tiles in turn
@@ -124,7 +126,6 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
   const int b = rest / a.Hq, h = rest % a.Hq, hk = h / (a.Hq / a.Hkv);
 
   pdl_wait();
-  pdl_launch_dependents();
   const int q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1);
   const int k0 = __ldg(a.kv_start + b), k1 = __ldg(a.kv_start + b + 1);
   const bool bad_rows = q0 < 0 || q1 < q0 || q1 > a.Nq || k0 < 0 || k1 < k0 || k1 > a.Nkv || q1 - q0 > a.max_q;
@@ -132,12 +133,12 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
     if (tid == 0 && h == 0 && qt == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
     return;
   }
-  const int nq = q1 - q0, n_k = k1 - k0, first = qt * 2 * kRows;
+  const int nq = q1 - q0, n_k = k1 - k0, first = qt * kW * kRows;
   if (first >= nq) return;
   // key tiles that each tile of queries sees: up to its last row's last key
-  int nt[2];
+  int nt[2] = {0, 0};
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
+  for (int w = 0; w < kW; ++w) {
     const int begin = first + w * kRows, last = min(nq, begin + kRows) - 1;  // last row
     const long long seen = begin < nq ? (long long)last + n_k - nq + 1 : 0;
     nt[w] = seen > 0 ? (int)((min(seen, (long long)n_k) + kRows - 1) / kRows) : 0;
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
       mbar_init(&o_full[w], 1);
       mbar_init(&drain[w], 1);
     }
-    mbar_init(partial, (nt[0] == tiles) + (nt[1] == tiles));
+    mbar_init(partial, (nt[0] == tiles) + (kW == 2 && nt[1] == tiles));
     mbar_init(tail, 1);
     fence_barrier_init();
   }
@@ -170,10 +171,15 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Only now: a kernel that starts while this CTA has no tensor memory yet could take all of it
+  // and then wait for this kernel to end.
+  pdl_launch_dependents();
   const uint32_t tmem = tmem_slot;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // (the shares add up to what the block was launched with: 3 x 168, or 2 x 128)
+    if (kW == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // -------------------------------------------------------------- producer
       if (elect_one()) {
@@ -191,14 +197,14 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
         uint32_t vp = 0;  // parity of the half's current use
         bool ok = true;
         for (int i = 0; ok && i < tiles; ++i) {
-          const int row = k0 + i * kRows, ks = i & 1;
+          const int row = k0 + i * kRows, ks = i % kKeySlots;
           if (i == 0 && half[0]) load_q(0);
-          if (i >= kKeySlots && !(ok = mbar_wait_bounded(&k_empty[ks], (uint32_t)((i >> 1) & 1) ^ 1u, a.dev_status))) break;
+          if (i >= kKeySlots && !(ok = mbar_wait_bounded(&k_empty[ks], (uint32_t)(i / kKeySlots & 1) ^ 1u, a.dev_status))) break;
           mbar_arrive_expect_tx(&k_full[ks], kKeys + (pos ? kAtom : 0u));
           tma_load_3d(smem + lay.k + (uint32_t)ks * kKeys, &p.mk, 0, row, hk * 2, &k_full[ks], keep);
           ++nkl;
           if (pos) {  // (its one slot is free when the last tile's keys are)
-            if (i > 0) ok = mbar_wait_bounded(&k_empty[ks ^ 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
+            if (i > 0) ok = mbar_wait_bounded(&k_empty[(i - 1) % kKeySlots], (uint32_t)((i - 1) / kKeySlots & 1), a.dev_status);
             tma_load_2d(smem + lay.pe, &p.mp, 0, row, &k_full[ks], keep);  // (after a timeout too: it is expected)
             if (!ok) break;
           }
@@ -216,12 +222,13 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
         if (tiles > 0) {
           for (int w = 0; w < 2; ++w)
             if (half[w]) mbar_wait_bounded(&q_full[w], 0, nullptr);
-          for (int j = max(0, nkl - 2); j < nkl; ++j) mbar_wait_bounded(&k_full[j & 1], (uint32_t)((j >> 1) & 1), nullptr);
+          for (int j = max(0, nkl - kKeySlots); j < nkl; ++j)
+            mbar_wait_bounded(&k_full[j % kKeySlots], (uint32_t)(j / kKeySlots & 1), nullptr);
           for (int j = max(0, nvl / 2 - 2); j < nvl / 2; ++j)
             mbar_wait_bounded(&v_full[j & 1], (uint32_t)((j >> 1) & 1), nullptr);
         }
       }
-    } else if (warp == 1 || warp == 3) {
+    } else if (warp == 1 || (kW == 2 && warp == 3)) {
       // -------------------------------------------------------------- MMA issuers, one a query tile
       // (one thread for both spent a third of its time testing barriers, which costs hundreds of
       // cycles while the products read shared memory, and kept the other tile's products waiting)
@@ -236,9 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
         const int pe_steps = a.dr / 16;
         int va = 0;
         auto issue_s = [&](int i) -> bool {
-          if (!mbar_wait_bounded(&k_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status)) return false;
+          if (!mbar_wait_bounded(&k_full[i % kKeySlots], (uint32_t)(i / kKeySlots & 1), a.dev_status)) return false;
           tc_fence_after();
-          const uint64_t dk = sw128_desc(k_addr + (uint32_t)(i & 1) * kKeys);
+          const uint64_t dk = sw128_desc(k_addr + (uint32_t)(i % kKeySlots) * kKeys);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma_bf16(s_col, dq + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2, dk + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2,
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
           for (int kk = 0; kk < pe_steps; ++kk)
             umma_bf16(s_col, dq + 2 * (kAtom >> 4) + 2 * kk, dp + 2 * kk, id_s, 1);
           umma_commit(&s_full[w]);
-          umma_commit(&k_empty[i & 1]);
+          umma_commit(&k_empty[i % kKeySlots]);
           return true;
         };
         bool ok = mbar_wait_bounded(&q_full[w], 0, a.dev_status) && issue_s(0);
@@ -300,7 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
     }
   } else {
     // ---------------------------------------------------------------- softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if (kW == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int w = (warp - 4) >> 2, quad = warp & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t s_col = tmem + lanes + (uint32_t)w * 128u, o_col = tmem + lanes + kOCol + (uint32_t)w * 128u;
@@ -422,19 +430,22 @@ __global__ void __launch_bounds__(kThreads, 1) stief_prefill_kernel(const __grid
   }
 }
 
-cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
+namespace {
+
+template <int kW>
+cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
   Args p{};
   p.a = a;
   p.atoms = a.dr > 0 ? 3 : 2;
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
-  for (p.nv = kMaxHalves; layout_of(p.atoms, p.nv).total > kMost;) --p.nv;
-  p.qtiles = (a.max_q + 2 * kRows - 1) / (2 * kRows);
+  for (p.nv = kW == 1 ? 2 : kMaxHalves; layout_of<kW>(p.atoms, p.nv).total > kMost;) --p.nv;
+  p.qtiles = (a.max_q + kW * kRows - 1) / (kW * kRows);
   p.scale2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
   if (p.scale2 < 1e-30f) p.scale2 = 1e-30f;  // above 0, so that a masked score stays -inf
   p.negate = a.scale < 0;
   const long long blocks = (long long)p.qtiles * a.Hq * a.B;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const uint32_t smem = layout_of(p.atoms, p.nv).total;
+  const uint32_t smem = layout_of<kW>(p.atoms, p.nv).total;
   const uint64_t rows = a.Nkv > 0 ? a.Nkv : 1;  // (no keys: the maps are never used)
   const void* k = a.Nkv > 0 ? a.k : a.q;
   const void* v = a.Nkv > 0 ? a.v : a.q;
@@ -445,20 +456,29 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
       !encode_tiled_bf16_3d(&p.mv, v, {64, rows, dk / 64}, {dk * 2, 128}, {64, kRows / 2, 2}) ||
       !encode_tiled_bf16_2d(&p.mp, pe, dp, a.dr > 0 ? rows : 1, dp * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  const auto kern = stief_prefill_kernel<kW>;
   static SmemLimit limit;
-  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_prefill_kernel), a.device, (int)smem);
+  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kern), a.device, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kW == 2 ? 384 : 256);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, stief_prefill_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
+  // Without a position part a CTA of one tile of queries takes 97 KB, and two of them share an SM:
+  // one's start and end overlap the other's products.  With it only one CTA fits, of two tiles.
+  return a.dr > 0 ? launch<2>(a, stream) : launch<1>(a, stream);
 }
 
 }  // namespace stief

@@ -40,7 +40,11 @@ namespace stief {
 
 namespace {
 
-constexpr int kTile = 64;           // tokens per tile
+// 64 tokens a tile (with 32, 82 against 76 us for 64 ragged sequences of up to 4096 tokens at 128
+// heads, 47 against 37 us for 128 of 2000 at rank 256: a tile's fixed costs outweigh the deeper
+// ring).
+constexpr int kTok = 64;
+constexpr uint32_t kAtom = kTok * 128;  // bytes of one 64-column atom of a tile
 constexpr int kMaxHeads = 64;       // heads per CTA
 constexpr int kMaxStages = 8;
 constexpr int kThreads = 256;
@@ -67,10 +71,10 @@ struct Args {
 struct Layout {
   uint32_t stages, p, ml, bars, total;
 };
-__host__ __device__ inline Layout layout_of(int na, int sa, int NH, int nstage, int tile) {
+__host__ __device__ inline Layout layout_of(int na, int sa, int NH, int nstage) {
   Layout l;
   l.stages = (uint32_t)na * NH * 128;  // q~ comes first
-  l.p = l.stages + (uint32_t)nstage * sa * tile * 128;
+  l.p = l.stages + (uint32_t)(nstage * sa) * kAtom;
   l.ml = l.p + (uint32_t)NH * 128;
   l.bars = l.ml + 3 * kMaxHeads * 4;
   l.total = l.bars + 8 * (4 * kMaxStages + 16);
@@ -101,7 +105,6 @@ struct Ring {
 
 __device__ __forceinline__ int valid_length(int L, int most) { return L < 0 || L > most ? 0 : L; }
 
-template <int kTok>
 __device__ __forceinline__ int tiles_of(int L) { return (L + kTok - 1) / kTok; }
 
 // Tiles are dealt out by cost: a sequence counts kSegment tiles more than it has, for the query's
@@ -117,7 +120,6 @@ struct Segment {
 // Walks the CTA's tiles sequence by sequence; every warp role walks the same way.  `skip`: what is
 // left of the sequence's extra cost, `off`: its next tile, `left`: what is left of the CTA's share,
 // which begins at `at`.
-template <int kTok>
 struct Walk {
   const int32_t* lens;
   int most, B, b, off, skip;
@@ -125,7 +127,7 @@ struct Walk {
   bool first = true;
   __device__ bool next(Segment& s) {
     while (left > 0 && b < B) {
-      const int L = valid_length(__ldg(lens + b), most), n = tiles_of<kTok>(L);
+      const int L = valid_length(__ldg(lens + b), most), n = tiles_of(L);
       if (n == 0 || skip >= left) {
         if (n > 0) return false;
         ++b;
@@ -153,17 +155,15 @@ struct Walk {
 
 }  // namespace
 
-template <int kTok>
 __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const __grid_constant__ Args p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sum[8], start_b, start_off;
-  constexpr int kAtom = kTok * 128;  // bytes of one 64-column atom of a tile
   const SharedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = (int)blockIdx.x % p.groups, cta = (int)blockIdx.x / p.groups;
   const int h_base = group * p.NH, nheads = min(p.NH, a.Hq - h_base);
-  const Layout lay = layout_of(p.na, p.sa, p.NH, p.nstage, kTok);
+  const Layout lay = layout_of(p.na, p.sa, p.NH, p.nstage);
   float* sm_f = reinterpret_cast<float*>(smem + lay.ml);  // rescale factors
   float* sm_m = sm_f + kMaxHeads;
   float* sm_l = sm_m + kMaxHeads;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   // where this CTA's tiles begin: a prefix sum of the sequences' tile counts
   const int per_thread = (a.B + kThreads - 1) / kThreads, c0 = tid * per_thread, c1 = min(a.B, c0 + per_thread);
   auto cost_of = [&](int b) {
-    const int n = tiles_of<kTok>(valid_length(__ldg(a.seq_lens + b), a.max_seq_len));
+    const int n = tiles_of(valid_length(__ldg(a.seq_lens + b), a.max_seq_len));
     return n > 0 ? n + kSegment : 0;
   };
   int sum = 0;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   }
   __syncthreads();
   const uint32_t tmem = tmem_slot;
-  Walk<kTok> walk{a.seq_lens, a.max_seq_len, a.B, count > 0 ? start_b : 0, count > 0 ? max(0, start_off) : 0,
+  Walk walk{a.seq_lens, a.max_seq_len, a.B, count > 0 ? start_b : 0, count > 0 ? max(0, start_off) : 0,
                   count > 0 ? max(0, -start_off) : 0, count, g0};
   Segment seg;
 
@@ -386,15 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
           if (!(ok = mbar_wait_bounded(&p_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status))) break;
           tc_fence_after();
           uint64_t dt = sw128_mn_desc(stage0 + (uint32_t)ring.st * stage_bytes, kAtom);
-          const uint64_t dp = sw128_desc(p_addr + (kTok == 32 ? (uint32_t)(i & 1) * 64u : 0u));
+          const uint64_t dp = sw128_desc(p_addr);
           for (int m = 0; m < p.nm; ++m, dt += 2 * kAtom >> 4) {
             const uint32_t d = tmem + (uint32_t)(m * p.NH);
             umma_bf16(d, dt, dp, id_o, t > seg.t0);
             umma_bf16(d, dt + 128, dp + 2, id_o, 1);
-            if (kTok == 64) {
-              umma_bf16(d, dt + 256, dp + 4, id_o, 1);
-              umma_bf16(d, dt + 384, dp + 6, id_o, 1);
-            }
+            umma_bf16(d, dt + 256, dp + 4, id_o, 1);
+            umma_bf16(d, dt + 384, dp + 6, id_o, 1);
             if (m == p.m0 - 1) umma_commit(&empty[2 * ring.st]);
           }
           if (pieces > 1) umma_commit(&empty[2 * ring.st + 1]);
@@ -511,17 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
             l0 += bf16lo(w[2 * j]) + bf16hi(w[2 * j]);
             l1 += bf16lo(w[2 * j + 1]) + bf16hi(w[2 * j + 1]);
           }
-          // P's buffer is free once the product of the last tile that used it is in: rows of 128
-          // bytes hold one tile of 64 tokens, or two of 32 in turn
-          constexpr int kBack = 64 / kTok;
-          if (i >= kBack &&
-              !mbar_wait_bounded(&pv_done[(i - kBack) & 1], (uint32_t)(((i - kBack) >> 1) & 1), a.dev_status))
+          // P's buffer is free once the last tile's product is in
+          if (i >= 1 && !mbar_wait_bounded(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status))
             bad = true;
           const uint32_t base = (uint32_t)r0 * 128u + (uint32_t)col * 2u;
-          const int j0 = kTok == 32 ? (i & 1) * 4 : 0;
 #pragma unroll
           for (int j = 0; j < kTok / 8; ++j) {
-            const uint32_t off = (uint32_t)(((j0 + j) ^ (r0 & 7)) << 4);
+            const uint32_t off = (uint32_t)((j ^ (r0 & 7)) << 4);
             *reinterpret_cast<uint32_t*>(smem + lay.p + base + off) = w[2 * j];
             *reinterpret_cast<uint32_t*>(smem + lay.p + base + 8 * 128 + off) = w[2 * j + 1];
           }
@@ -547,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       if (!bad) bad = !mbar_wait_bounded(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
       if (named_bar_or(1, 128, bad)) break;
       tc_fence_after();
-      const int n = tiles_of<kTok>(seg.L);
+      const int n = tiles_of(seg.L);
       const bool whole = seg.t0 == 0 && seg.t1 == n;
       const int dim = quad * 32 + lane;
       const int slot = ((int)blockIdx.x * 2 + (seg.first ? 0 : 1));
@@ -730,10 +724,9 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   p.G = ctas / p.groups;
   p.scale2 = a.scale * 1.4426950408889634f;
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
-  const int tile = kTile;
-  for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage, tile).total > kMost;)
+  for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage).total > kMost;)
     --p.nstage;
-  uint32_t smem = layout_of(p.na, p.sa, p.NH, p.nstage, tile).total;
+  uint32_t smem = layout_of(p.na, p.sa, p.NH, p.nstage).total;
   if (smem > kMost) return cudaErrorInvalidValue;
   if (smem < 120u * 1024u) smem = 120u * 1024u;  // one CTA an SM: it holds all of TMEM
   const uint64_t rows = (uint64_t)a.num_pages * a.page_size, pitch = (uint64_t)p.w * 2;
@@ -748,16 +741,16 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   const uint32_t n1 = (uint32_t)(p.na - p.n0);
   if (p.whole_rows) {
     if (!encode_tiled_bf16_3d(&p.ma, a.pages, {64, rows, (uint64_t)p.na}, {pitch, 128},
-                              {64, (uint32_t)tile, (uint32_t)p.n0}) ||
+                              {64, kTok, (uint32_t)p.n0}) ||
         !encode_tiled_bf16_3d(&p.mb, a.pages, {64, rows, (uint64_t)p.na}, {pitch, 128},
-                              {64, (uint32_t)tile, n1 > 0 ? n1 : 1u}))
+                              {64, kTok, n1 > 0 ? n1 : 1u}))
       return cudaErrorInvalidValue;
   } else {
-    if (!encode_tiled_bf16_2d(&p.ma, a.pages, (uint64_t)p.w, rows, pitch, 64, (uint32_t)tile, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_tiled_bf16_2d(&p.ma, a.pages, (uint64_t)p.w, rows, pitch, 64, kTok, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
     p.mb = p.ma;
   }
-  const auto kern = stief_shared_decode_kernel<kTile>;
+  const auto kern = stief_shared_decode_kernel;
   static SmemLimit limit;
   cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kern), a.device, (int)smem);
   if (e != cudaSuccess) return e;
