@@ -398,7 +398,10 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
       tc_fence_after();
       const uint64_t ls = add2(l0, l1);
       const float inv = seen > 0 ? 1.f / (lo_of(ls) + hi_of(ls)) : 0.f;
-      uint16_t* out = a.out + ((size_t)(q0 + row) * a.Hq + h) * 128;
+      // The rows go through the warp's part of the queries' memory (their last product is done), so
+      // that half a warp stores a whole row: stored by the thread that holds it, in pieces of 16
+      // bytes, a row took five times as long.  A row's 16-byte pieces are rotated by its number.
+      uint8_t* stage = smem + (uint32_t)(w * p.atoms) * kAtom + (uint32_t)quad * 32 * 256;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t v[32];
@@ -406,19 +409,25 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
           tmem_ld32(o_col + c, v);
           tmem_wait_ld();
         }
-        if (row < nq) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (seen > 0) {
-              x.x = pack_bf16x2_rn(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
-              x.y = pack_bf16x2_rn(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
-              x.z = pack_bf16x2_rn(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
-              x.w = pack_bf16x2_rn(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
-            }
-            *reinterpret_cast<uint4*>(out + c + e) = x;
+        for (int e = 0; e < 32; e += 8) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (seen > 0) {
+            x.x = pack_bf16x2_rn(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
+            x.y = pack_bf16x2_rn(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+            x.z = pack_bf16x2_rn(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
+            x.w = pack_bf16x2_rn(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
           }
+          *reinterpret_cast<uint4*>(stage + lane * 256 + ((((c + e) >> 3) ^ (lane & 15)) << 4)) = x;
         }
+      }
+      __syncwarp();
+      const int row0 = row - lane, piece = lane & 15;
+      uint16_t* out = a.out + ((size_t)(q0 + row0) * a.Hq + h) * 128 + piece * 8;
+#pragma unroll
+      for (int r = lane >> 4; r < 32; r += 2) {
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 256 + ((piece ^ (r & 15)) << 4));
+        if (row0 + r < nq) *reinterpret_cast<uint4*>(out + (size_t)r * a.Hq * 128) = x;
       }
     }
   }
