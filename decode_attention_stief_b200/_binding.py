@@ -139,8 +139,32 @@ def library() -> ctypes.CDLL:
             lib.stief_read_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
             lib.stief_status_string.restype = ctypes.c_char_p
             lib.stief_status_string.argtypes = [_i]
+            _load_marshal(lib)
             _lib = lib
     return _lib
+
+
+_marshal = None  # the extension of csrc/marshal.cpp, once the library is loaded
+
+
+def _load_marshal(lib) -> None:
+    """Loads the extension that makes the newer calls without their checks in Python, if it has
+    been built, and gives it the library's addresses."""
+    global _marshal
+    try:
+        from . import _marshal as m
+    except ImportError:
+        return
+    m.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+             for n in ("stief_plan_pages", "stief_append_shared_paged", "stief_decode_shared_paged",
+                       "stief_expand_shared_paged", "stief_prefill_attention")))
+    _marshal = m
+
+
+def _short_way(stream) -> bool:
+    """Whether a call may go through the extension: it knows the current stream only, and
+    prepare() wants the arguments, not the call."""
+    return _marshal is not None and stream is None and getattr(_capture, "calls", None) is None
 
 
 def _check(func: str, code: int) -> None:
@@ -861,9 +885,9 @@ def plan_workspace(device="cuda") -> torch.Tensor:
     return torch.zeros(stief_plan_workspace_bytes(), dtype=torch.uint8, device=device)
 
 
-# The calls below cost the host several microseconds of Python each, which a decode step pays
-# many times over, so their checks take the short way when everything is as it should be: one
-# test a tensor, and the long way (which says what is wrong) only when it fails.
+# The calls below first try the extension (_marshal): it makes the call if every argument is as it
+# should be, and returns None otherwise.  What follows in each function is the whole check, which
+# says what is wrong, and the way for other streams, prepare(), and an extension that is not built.
 
 def _here(t, name, dtype, ndim, dev):
     """Data pointer of a contiguous `ndim`-dimensional tensor of `dtype` on device `dev`, the
@@ -873,6 +897,11 @@ def _here(t, name, dtype, ndim, dev):
         return t.data_ptr()
     _dev(t, name, dtype, ndim)
     raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _current():
+    """The current device's number; -2, which no tensor has, without a GPU."""
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
 
 
 def _ws(workspace, dev):
@@ -903,7 +932,13 @@ def stief_plan_pages(new_tokens, seq_lens, block_table, free_pages, free_count, 
     kv_start [B + 1], seq_lens_out [B] (each written, or None); free_count_out [1].  All int32.
     seq_lens_out may be seq_lens and free_count_out may be free_count.
     """
-    dev, i32 = torch.cuda.current_device(), torch.int32
+    if _short_way(stream):
+        code = _marshal.plan_pages(new_tokens, seq_lens, block_table, free_pages, free_count, slots, q_start,
+                                   kv_start, seq_lens_out, free_count_out, workspace, page_size, dev_status)
+        if code is not None:
+            _check("stief_plan_pages", code)
+            return
+    dev, i32 = _current(), torch.int32
     pn, pl = _here(new_tokens, "new_tokens", i32, 1, dev), _here(seq_lens, "seq_lens", i32, 1, dev)
     pt, pf = _here(block_table, "block_table", i32, 2, dev), _here(free_pages, "free_pages", i32, 1, dev)
     pc, po = _here(free_count, "free_count", i32, 1, dev), _here(free_count_out, "free_count_out", i32, 1, dev)
@@ -953,7 +988,12 @@ def stief_append_shared_paged(c_new, pe_new, slots, pages,
     position part), rows contiguous, any row stride that is a multiple of 8; slots [N] int32;
     pages [num_pages][page_size][r + dr] bf16.
     """
-    dev = torch.cuda.current_device()
+    if _short_way(stream):
+        code = _marshal.append_shared_paged(c_new, pe_new, slots, pages, dev_status)
+        if code is not None:
+            _check("stief_append_shared_paged", code)
+            return
+    dev = _current()
     pc, N, r, sc = _rows(c_new, "c_new", dev)
     pp, n_pe, dr, sp = (None, N, 0, 0) if pe_new is None else _rows(pe_new, "pe_new", dev)
     psl = _here(slots, "slots", torch.int32, 1, dev)
@@ -986,7 +1026,13 @@ def stief_decode_shared_paged(q, pages, block_table, seq_lens, out, workspace, m
     q [B][Hq][r + dr], pages [num_pages][page_size][r + dr], out [B][Hq][r] (written), bf16;
     block_table [B][max_pages], seq_lens [B] int32; workspace from shared_workspace_for.
     """
-    dev, b16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
+    if _short_way(stream):
+        code = _marshal.decode_shared_paged(q, pages, block_table, seq_lens, out, workspace, max_seq_len, scale,
+                                            dev_status)
+        if code is not None:
+            _check("stief_decode_shared_paged", code)
+            return out
+    dev, b16, i32 = _current(), torch.bfloat16, torch.int32
     pq, ppg = _here(q, "q", b16, 3, dev), _here(pages, "pages", b16, 3, dev)
     pt, psl = _here(block_table, "block_table", i32, 2, dev), _here(seq_lens, "seq_lens", i32, 1, dev)
     po = _here(out, "out", b16, 3, dev)
@@ -1012,7 +1058,12 @@ def stief_expand_shared_paged(pages, block_table, kv_start, W_K, W_V, k, v, k_pe
     (None, or with dr = 0, for rows without a position part) bf16; block_table [B][max_pages],
     kv_start [B + 1] int32.
     """
-    dev, b16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
+    if _short_way(stream):
+        code = _marshal.expand_shared_paged(pages, block_table, kv_start, W_K, W_V, k, v, k_pe, dev_status)
+        if code is not None:
+            _check("stief_expand_shared_paged", code)
+            return
+    dev, b16, i32 = _current(), torch.bfloat16, torch.int32
     ppg, pt = _here(pages, "pages", b16, 3, dev), _here(block_table, "block_table", i32, 2, dev)
     pst = _here(kv_start, "kv_start", i32, 1, dev)
     pwk, pwv = _here(W_K, "W_K", b16, 3, dev), _here(W_V, "W_V", b16, 3, dev)
@@ -1039,7 +1090,12 @@ def stief_prefill_attention(q, k, v, q_start, kv_start, out, max_q_len: int, sca
     q [Nq][Hq][d + dr], k and v [Nkv][Hkv][d], k_pe [Nkv][dr] (None when dr = 0), out
     [Nq][Hq][d] (written), bf16; q_start, kv_start [B + 1] int32.
     """
-    dev, b16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
+    if _short_way(stream):
+        code = _marshal.prefill_attention(q, k, v, q_start, kv_start, out, max_q_len, scale, k_pe, dev_status)
+        if code is not None:
+            _check("stief_prefill_attention", code)
+            return out
+    dev, b16, i32 = _current(), torch.bfloat16, torch.int32
     pq, pk = _here(q, "q", b16, 3, dev), _here(k, "k", b16, 3, dev)
     pv, po = _here(v, "v", b16, 3, dev), _here(out, "out", b16, 3, dev)
     pqs, pks = _here(q_start, "q_start", i32, 1, dev), _here(kv_start, "kv_start", i32, 1, dev)

@@ -8,6 +8,10 @@ statically so the library loads beside any torch build.
 same sources with ``-DSTIEF_TEST_HOOKS``: bounded waits that give up after 50 ms
 and two test-only exports (a setup-barrier stall that makes the waits run out,
 the address of the no-allocation scratch).  Only the timeout tests load it.
+
+``build_marshal()`` builds ``_marshal.so`` with g++: a CPython extension that takes
+torch tensors to the library's calls without the cost of doing so in Python.  The
+binding works without it, more slowly.
 """
 from __future__ import annotations
 
@@ -83,6 +87,36 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
     return lib
 
 
+MARSHAL = os.path.join(PKG, "_marshal.so")
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/marshal.cpp against the running Python and torch."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "marshal.cpp")
+    deps = [src, os.path.join(ROOT, "include", "stief.h"), torch.__file__]
+    if not force and os.path.exists(MARSHAL) \
+            and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
+        return MARSHAL
+    home = os.path.dirname(torch.__file__)
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_path("include"),
+           "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           src, "-o", tmp, "-L", os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 if __name__ == "__main__":
     print(build_library(force="--force" in sys.argv, verbose=True,
                         variant="testhooks" if "--testhooks" in sys.argv else None))
+    print(build_marshal(force="--force" in sys.argv, verbose=True))

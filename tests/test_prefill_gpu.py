@@ -229,3 +229,36 @@ def test_plan_drives_the_paged_fused_step():
     for _ in range(steps):
         want, _, _, _, have, left, _ = plan_reference(new, have, want, free.tolist(), left, ps)
     assert np.array_equal(table.cpu().numpy(), want)
+
+
+def test_both_ways_into_the_library():
+    """The binding's two ways (the extension, and Python: other streams, prepare) make the same
+    call, and refuse the same arguments for the same reasons."""
+    q, k, v, pe = _inputs([130], [130], 4, 2, 16, 21)
+    qs, out = _i([0, 130]), [torch.zeros((130, 4, 128), dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+    stief.stief_prefill_attention(q, k, v, qs, qs, out[0], 130, 0.1, k_pe=pe)
+    stief.stief_prefill_attention(q, k, v, qs, qs, out[1], 130, 0.1, k_pe=pe, stream=torch.cuda.current_stream())
+    call = stief.prepare(stief.stief_prefill_attention, q, k, v, qs, qs, out[2], 130, 0.1, k_pe=pe)
+    assert int(out[2].count_nonzero()) == 0  # prepared, not called
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+    for stream in (None, torch.cuda.current_stream()):
+        for bad, error in ((dict(q=q.float()), TypeError), (dict(k=k.transpose(0, 1)), ValueError),
+                           (dict(v=v[:, :1].contiguous()), ValueError), (dict(qs=qs.cpu()), ValueError),
+                           (dict(qs=qs[:1]), ValueError), (dict(out=out[0][:5]), ValueError), (dict(out=None), TypeError),
+                           (dict(scale=float("nan")), stief.StiefError), (dict(most=-1), stief.StiefError)):
+            a = dict(q=q, k=k, v=v, qs=qs, out=out[0], most=130, scale=0.1)
+            a.update(bad)
+            with pytest.raises(error):
+                stief.stief_prefill_attention(a["q"], a["k"], a["v"], a["qs"], qs, a["out"], a["most"], a["scale"],
+                                              k_pe=pe, stream=stream)
+        pool, table = torch.zeros((3, 64, 48), dtype=torch.bfloat16, device=DEV), _i([[0, 1]])
+        ql, ol, ln = (torch.zeros(s, dtype=torch.bfloat16, device=DEV) for s in ((1, 4, 48), (1, 4, 32), (1,)))
+        ws = stief.shared_workspace_for(1, 4, 32)
+        for bad, error in ((dict(ln=ln), TypeError), (dict(ws=ws[:8]), stief.StiefError), (dict(most=129), stief.StiefError),
+                           (dict(ol=ol[:, :3].contiguous()), ValueError)):
+            a = dict(ln=_i([5]), ws=ws, most=100, ol=ol)
+            a.update(bad)
+            with pytest.raises(error):
+                stief.stief_decode_shared_paged(ql, pool, table, a["ln"], a["ol"], a["ws"], a["most"], 0.1, stream=stream)

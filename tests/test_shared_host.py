@@ -106,3 +106,22 @@ def test_workspace_sizes(lib):
     for bad in ((0, 32, 512), (1, 0, 512), (1, 257, 512), (1, 32, 8), (1, 32, 528)):
         assert stief.stief_decode_shared_workspace_bytes(*bad) == 0
     assert ctypes.sizeof(ctypes.c_size_t) == 8
+
+
+def test_binding_refuses_before_any_cuda_call():
+    """Wrong types and CPU tensors are refused with the reason, with or without a GPU."""
+    import torch
+    i = torch.zeros(4, dtype=torch.int32)
+    b = torch.zeros((2, 64, 48), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="new_tokens must be on a CUDA device"):
+        stief.stief_plan_pages(i, i, i.view(2, 2), i, i[:1], None, None, None, None, i[:1], i, 64)
+    with pytest.raises(TypeError, match="seq_lens|new_tokens"):
+        stief.stief_plan_pages(i.float(), i, i.view(2, 2), i, i[:1], None, None, None, None, i[:1], i, 64)
+    with pytest.raises((ValueError, TypeError), match="c_new"):
+        stief.stief_append_shared_paged(b[0], None, i, b)
+    with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+        stief.stief_decode_shared_paged(None, b, i, i, b, i, 3, 0.1)
+    with pytest.raises(ValueError, match="pages must be on a CUDA device"):
+        stief.stief_expand_shared_paged(b, i, i, b, b, b, b)
+    with pytest.raises(ValueError, match="q must be on a CUDA device"):
+        stief.stief_prefill_attention(b, b, b, i, i, b, 3, 0.1)
