@@ -10,7 +10,7 @@
 
 namespace {
 
-constexpr int kMaxPlanSequences = 8192;  // the plan keeps 24 bytes a sequence in shared memory
+constexpr int kMaxPlanSequences = 8192;  // the plan keeps 28 bytes a sequence in shared memory
 constexpr int kPageQuantum = 64;
 constexpr size_t kPlanWorkspace = 256;
 

@@ -65,6 +65,7 @@ struct Args {
   int NH, groups, G;  // heads per CTA (a multiple of 16), head groups, CTAs per group
   int nstage;
   int whole_rows;     // w % 64 == 0: one copy brings a tile's atoms
+  int whole;          // sequences are not split over CTAs, and there is no second kernel
   float scale2;       // scale * log2(e)
 };
 
@@ -110,6 +111,7 @@ __device__ __forceinline__ int tiles_of(int L) { return (L + kTok - 1) / kTok; }
 // Tiles are dealt out by cost: a sequence counts kSegment tiles more than it has, for the query's
 // copy and the output, placed before its first tile.
 constexpr int kSegment = 3;
+constexpr int kWholeTiles = 4;
 
 // The stretch of one sequence's tiles [t0, t1) that a CTA works on.
 struct Segment {
@@ -124,21 +126,22 @@ struct Walk {
   const int32_t* lens;
   int most, B, b, off, skip;
   long long left, at;
+  bool whole;    // sequences are not split: the CTA takes those that begin in its share
   bool first = true;
   __device__ bool next(Segment& s) {
     while (left > 0 && b < B) {
       const int L = valid_length(__ldg(lens + b), most), n = tiles_of(L);
-      if (n == 0 || skip >= left) {
-        if (n > 0) return false;
+      if (n == 0) {
         ++b;
         continue;
       }
+      if (skip >= left && !whole) return false;
       left -= skip;
       at += skip;
       s.b = b;
       s.L = L;
       s.t0 = off;
-      s.t1 = (int)min((long long)n, off + left);
+      s.t1 = whole ? n : (int)min((long long)n, off + left);
       s.at = at;
       s.first = first;
       first = false;
@@ -250,11 +253,24 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     }
     start_b = b;
     start_off = (int)(g0 - at) - kSegment;  // negative: cost before the first tile
+    if (p.whole && g0 > at) {  // that sequence is another CTA's: begin with the next
+      start_b = b + 1;
+      start_off = -kSegment - (at + cost_of(b) - (int)g0);
+    }
   }
   __syncthreads();
   const uint32_t tmem = tmem_slot;
-  Walk walk{a.seq_lens, a.max_seq_len, a.B, count > 0 ? start_b : 0, count > 0 ? max(0, start_off) : 0,
-                  count > 0 ? max(0, -start_off) : 0, count, g0};
+  Walk walk{a.seq_lens, a.max_seq_len, a.B, 0, 0, 0, count, g0, p.whole != 0};
+  if (count > 0) {
+    walk.b = start_b;
+    walk.off = max(0, start_off);
+    walk.skip = max(0, -start_off);
+  }
+  if (p.whole && count > 0) {  // (what lies before the first sequence of the share is another's)
+    walk.left -= walk.skip - kSegment;
+    walk.at += walk.skip - kSegment;
+    walk.skip = kSegment;
+  }
   Segment seg;
 
   const int pieces = p.n0 < p.na ? 2 : 1;
@@ -587,13 +603,20 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       const int th = tid - 128;
       if (!whole && th < nheads) ml[th] = make_float2(sm_m[th], sm_l[th]);
       // the CTAs that hold this sequence, for the merge: written by the one with its first tile
-      if (seg.t0 == 0 && th == 0 && group == 0) {
+      if (seg.t0 == 0 && th == 0 && group == 0 && !p.whole) {
         reinterpret_cast<int2*>(ws)[seg.b] =
             make_int2(cta * 2 + (seg.first ? 0 : 1), whole ? -1 : (int)((seg.at + n - 1) / per));
       }
       named_bar_sync(1, 128);  // sm_l, sm_m and O~ have been read
       if (lane == 0) mbar_arrive(o_free);
     }
+    // without a second kernel the zeros of empty sequences are written here
+    if (p.whole)
+      for (int b = (int)blockIdx.x; b < a.B; b += (int)gridDim.x)
+        if (valid_length(__ldg(a.seq_lens + b), a.max_seq_len) == 0) {
+          uint4* out = reinterpret_cast<uint4*>(a.out + (size_t)b * a.Hq * a.r);
+          for (int e = tid - 128; e < a.Hq * a.r / 8; e += 128) out[e] = make_uint4(0, 0, 0, 0);
+        }
   }
   __syncwarp();
   tc_fence_before();
@@ -723,6 +746,9 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   const int ctas = a.sms < kMaxCtas ? a.sms : kMaxCtas;
   p.G = ctas / p.groups;
   p.scale2 = a.scale * 1.4426950408889634f;
+  // Short sequences are finished by one CTA each: the second kernel costs 2 us, as much as two
+  // further tiles.  (5 sequences of up to 200 tokens: 7.9 us with it.)
+  p.whole = a.max_seq_len <= kWholeTiles * kTok;
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
   for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage).total > kMost;)
     --p.nstage;
@@ -765,7 +791,7 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   // many parts a sequence: a CTA's warps share them; else a warp a head
