@@ -5,14 +5,17 @@
 // bounds it: 4 r H 128 operations a token on the tensor cores, or, for small r, the 512 H bytes
 // a token that it writes.
 //
-// A unit is 128 tokens of one sequence x one head: one accumulator of 128 x 256 in TMEM, two of
-// them in turn.  Units are dealt out evenly, in order, heads innermost: a CTA keeps its 128 rows
-// in shared memory (two row tiles where they fit) and streams the weights' 64-column chunks
-// through a ring, so a unit costs one pass over its head's weights from L2.
-//   warp 0: TMA producer; warp 1: MMA issuer (M = 128, N = 256); warps 4-7 store the keys,
-//   warps 8-11 the values, a thread a token: 32-byte stores, so that every store fills whole
-//   sectors (16-byte stores if an output is not 32-byte aligned).  The unit of head 0 also copies
-//   the position values.
+// Two CTAs on neighbouring SMs work as a pair: a unit is 256 tokens (a row tile of 128 in each
+// CTA) x one head, one product of M = 256, N = 256 with 256 accumulator columns in each CTA's
+// TMEM, two of them in turn.  Each CTA brings half of the head's weights, the first W_K[h], the
+// second W_V[h]: with both halves in one CTA (M = 128) the weights alone asked for 64 bytes a
+// cycle and SM from L2, and 4096 tokens x 32 heads took 36 us.  Units are dealt out evenly, in
+// order, heads innermost: a CTA keeps its rows in shared memory (two row tiles where they fit) and
+// streams the weights' 64-column chunks through a ring.
+//   warp 0: TMA producer; warp 1 of the first CTA: MMA issuer; warps 4-7 store the keys, warps 8-11
+//   the values, a thread a token: 32-byte stores, so that every store fills whole sectors (16-byte
+//   stores if an output is not 32-byte aligned).  The unit of head 0 also copies the position
+//   values.
 // Row tiles begin at multiples of 128 tokens of their sequence, hence at multiples of 64 rows of
 // a page: two copies bring 64 rows each.
 #include <cstdint>
@@ -25,9 +28,9 @@ namespace stief {
 
 namespace {
 
-constexpr int kRows = 128;                  // tokens a unit
+constexpr int kRows = 128;                  // tokens a row tile
 constexpr uint32_t kAtomA = kRows * 128;    // 128 rows x 64 columns
-constexpr uint32_t kStageB = 256 * 128;     // 256 weight rows x 64 columns
+constexpr uint32_t kStageB = 128 * 128;     // 128 weight rows x 64 columns
 constexpr int kThreads = 384;
 constexpr int kMaxStages = 6;
 constexpr uint32_t kTmemCols = 512;
@@ -59,43 +62,47 @@ __device__ __forceinline__ void rows_of(const SharedExpandArgs& a, int b, int& s
 }
 
 struct Unit {
-  int b, j, h;         // sequence, row tile of it, head
+  int b, j, h;         // sequence, row tile of it (none, for the second CTA at the end: len == 0), head
   int s0, len;         // first output row, rows of the sequence
   bool new_tile, last_of_tile;
 };
-// Walks a CTA's units; every warp role walks the same way.
+// Walks a CTA's units; every warp role of both CTAs walks the same way, the second CTA one row
+// tile further on.
 struct Walk {
   const SharedExpandArgs& a;
   int b, j, h;
   long long left;
   bool fresh = true;
-  __device__ bool next(Unit& u) {
-    while (left > 0 && b < a.B) {
+  // to the row tile `step` tiles on
+  __device__ void move(int step) {
+    j += step;
+    while (b < a.B) {
       int s0, s1;
       rows_of(a, b, s0, s1);
       const int n = (s1 - s0 + kRows - 1) / kRows;
-      if (j >= n) {
-        j = 0;
-        h = 0;
-        ++b;
-        continue;
-      }
-      u.b = b;
-      u.j = j;
-      u.h = h;
-      u.s0 = s0;
-      u.len = s1 - s0;
-      u.new_tile = fresh || h == 0;
-      fresh = false;
-      --left;
-      if (++h == a.H) {
-        h = 0;
-        ++j;
-      }
-      u.last_of_tile = h == 0 || left == 0;
-      return true;
+      if (j < n) return;
+      j -= n;
+      ++b;
     }
-    return false;
+  }
+  __device__ bool next(Unit& u) {
+    if (left <= 0) return false;
+    int s0 = 0, s1 = 0;
+    if (b < a.B) rows_of(a, b, s0, s1);
+    u.b = b;
+    u.j = j;
+    u.h = h;
+    u.s0 = s0;
+    u.len = s1 - s0;
+    u.new_tile = fresh || h == 0;
+    fresh = false;
+    --left;
+    if (++h == a.H) {
+      h = 0;
+      move(2);
+    }
+    u.last_of_tile = h == 0 || left == 0;
+    return true;
   }
 };
 
@@ -123,13 +130,16 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8], b
 
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const __grid_constant__ Args p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const __grid_constant__ Args p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sum[kThreads / 32], start_b, start_j;
   const SharedExpandArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Layout lay = layout_of(p.chunks, p.na, p.nb);
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  // (the full barriers and d_empty that count are the leader's; the others are each CTA's own)
   uint64_t* b_full = reinterpret_cast<uint64_t*>(smem + lay.bars);
   uint64_t* b_empty = b_full + kMaxStages;
   uint64_t* a_full = b_empty + kMaxStages;  // [2]
@@ -138,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
   uint64_t* d_empty = a_full + 6;           // [2] it has been read
   uint64_t* drain = a_full + 8;
 
-  if ((smem_u32(smem) & 1023u) != 0) {
+  if ((smem_u32(smem) & 1023u) != 0) {  // (the same in both CTAs)
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
     return;
   }
@@ -151,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
       mbar_init(&a_full[i], 1);
       mbar_init(&a_empty[i], 1);
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 8);
+      mbar_init(&d_empty[i], 16);
     }
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -159,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
     prefetch_tensormap(&p.mwk);
     prefetch_tensormap(&p.mwv);
   }
-  if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
+  if (warp == 1) tmem_alloc_pair(&tmem_slot, kTmemCols);
 
   pdl_wait();
   pdl_launch_dependents();
@@ -188,10 +198,11 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
     if (i == warp) incl += total_tiles;
     total_tiles += warp_sum[i];
   }
-  const long long total = (long long)total_tiles * a.H, per = (total + gridDim.x - 1) / gridDim.x;
-  const long long u0 = (long long)blockIdx.x * per;
+  const int pairs = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
+  const long long total = (long long)((total_tiles + 1) / 2) * a.H, per = (total + pairs - 1) / pairs;
+  const long long u0 = (long long)pair * per;
   const long long count = u0 >= total ? 0 : min(per, total - u0);
-  const int tile0 = (int)(u0 / a.H);
+  const int tile0 = 2 * (int)(u0 / a.H);
   if (count > 0 && tile0 >= incl - sum && tile0 < incl) {
     int at = incl - sum, b = c0;
     for (;; ++b) {
@@ -204,13 +215,18 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
     start_b = b;
     start_j = tile0 - at;
   }
-  __syncthreads();
+  // (also: the barriers of both CTAs are initialised, and both have their tensor memory)
+  cluster_sync();
   const uint32_t tmem = tmem_slot;
-  Walk walk{a, count > 0 ? start_b : 0, count > 0 ? start_j : 0, (int)(u0 - (long long)tile0 * a.H), count};
+  Walk walk{a, count > 0 ? start_b : 0, count > 0 ? start_j : 0, (int)(u0 - (long long)(tile0 / 2) * a.H), count};
+  if (count > 0 && !leader) walk.move(1);
   Unit u;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
+    // The leader expects both CTAs' bytes on its barriers.  (The second CTA's copies may land first:
+    // it asks for a slot only when the products with its last use are done, that is in the phase
+    // that the leader opens.)
     if (elect_one()) {
       const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
       Ring ra{p.na}, rb{p.nb};
@@ -219,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
       while (ok && walk.next(u)) {
         if (u.new_tile) {
           if (na >= p.na && !(ok = mbar_wait_bounded(&a_empty[ra.st], ra.ph ^ 1u, a.dev_status))) break;
-          mbar_arrive_expect_tx(&a_full[ra.st], (uint32_t)p.chunks * kAtomA);
+          const uint32_t bar = in_cta(&a_full[ra.st], 0);
+          if (leader) mbar_arrive_expect_tx(&a_full[ra.st], 2u * p.chunks * kAtomA);
           uint8_t* dst = smem + (uint32_t)(ra.st * p.chunks) * kAtomA;
           for (int half = 0; half < 2; ++half) {
             const int pos = u.j * kRows + half * 64, pi = pos / a.page_size;
@@ -228,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
             const int row = page >= 0 && page < a.num_pages ? page * a.page_size + pos % a.page_size
                                                             : a.num_pages * a.page_size;
             for (int c = 0; c < p.chunks; ++c)
-              tma_load_2d(dst + (uint32_t)c * kAtomA + half * (kAtomA / 2), &p.mc, 64 * c, row, &a_full[ra.st], once);
+              tma_load_2d_pair(dst + (uint32_t)c * kAtomA + half * (kAtomA / 2), &p.mc, 64 * c, row, bar, once);
           }
           ++na;
           ra.next();
@@ -236,21 +253,23 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
         for (int c = 0; c < p.chunks; ++c, ++nb, rb.next()) {
           if (nb >= p.nb && !(ok = mbar_wait_bounded(&b_empty[rb.st], rb.ph ^ 1u, a.dev_status))) break;
           uint8_t* dst = smem + lay.b + (uint32_t)rb.st * kStageB;
-          mbar_arrive_expect_tx(&b_full[rb.st], kStageB);
-          tma_load_2d(dst, &p.mwk, 64 * c, u.h * 128, &b_full[rb.st], keep);
-          tma_load_2d(dst + kStageB / 2, &p.mwv, 64 * c, u.h * 128, &b_full[rb.st], keep);
+          const uint32_t bar = in_cta(&b_full[rb.st], 0);
+          if (leader) mbar_arrive_expect_tx(&b_full[rb.st], 2 * kStageB);
+          tma_load_2d_pair(dst, leader ? &p.mwk : &p.mwv, 64 * c, u.h * 128, bar, keep);
         }
       }
-      // every requested copy lands before the shared memory is released
-      for (int k = max(0, na - p.na); k < na; ++k)
+      // every requested copy of both CTAs lands before their shared memory is released
+      if (leader)
+       for (int k = max(0, na - p.na); k < na; ++k)
         mbar_wait_bounded(&a_full[k % p.na], (uint32_t)((k / p.na) & 1), nullptr);
-      for (int k = max(0, nb - p.nb); k < nb; ++k)
+      if (leader)
+       for (int k = max(0, nb - p.nb); k < nb; ++k)
         mbar_wait_bounded(&b_full[k % p.nb], (uint32_t)((k / p.nb) & 1), nullptr);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    if (elect_one()) {
-      const uint32_t id = idesc_bf16_f32(128, 256, false, false);
+    if (leader && elect_one()) {
+      const uint32_t id = idesc_bf16_f32(256, 256, false, false);
       const uint32_t a_addr = smem_u32(smem), b_addr = smem_u32(smem + lay.b);
       Ring ra{p.na}, rb{p.nb};
       uint32_t d = 0, dp = 0;  // accumulator, parity of its use
@@ -270,21 +289,21 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
           const uint64_t db = sw128_desc(b_addr + (uint32_t)rb.st * kStageB);
           const int steps = min(4, (a.r - 64 * c) / 16);
           const uint32_t acc = tmem + d * 256u;
-          umma_bf16(acc, da, db, id, c > 0);
-          if (steps > 1) umma_bf16(acc, da + 2, db + 2, id, 1);
-          if (steps > 2) umma_bf16(acc, da + 4, db + 4, id, 1);
-          if (steps > 3) umma_bf16(acc, da + 6, db + 6, id, 1);
-          umma_commit(&b_empty[rb.st]);
+          umma_bf16_pair(acc, da, db, id, c > 0);
+          if (steps > 1) umma_bf16_pair(acc, da + 2, db + 2, id, 1);
+          if (steps > 2) umma_bf16_pair(acc, da + 4, db + 4, id, 1);
+          if (steps > 3) umma_bf16_pair(acc, da + 6, db + 6, id, 1);
+          umma_commit_pair(&b_empty[rb.st]);
         }
         if (!ok) break;
-        if (u.last_of_tile) umma_commit(&a_empty[st_a]);
-        umma_commit(&d_full[d]);
+        if (u.last_of_tile) umma_commit_pair(&a_empty[st_a]);
+        umma_commit_pair(&d_full[d]);
         d ^= 1u;
         if (d == 0) dp ^= 1u;
         ++n;
       }
       // (on the normal path the end of the last product, after a timeout a bounded chance to finish)
-      umma_commit(drain);
+      umma_commit_pair(drain);
       mbar_wait_bounded(drain, 0, nullptr);
     }
   } else if (warp >= 4) {
@@ -329,17 +348,17 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_expand_kernel(const 
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&d_empty[d]);
+      if (lane == 0) mbar_arrive_cluster_relaxed(in_cta(&d_empty[d], 0));
       d ^= 1u;
       if (d == 0) dp ^= 1u;
     }
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // neither CTA is read, written or signalled by the other any more
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
@@ -366,12 +385,12 @@ cudaError_t launch_shared_expand(const SharedExpandArgs& a, cudaStream_t stream)
   cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_shared_expand_kernel), a.device, (int)smem);
   if (e != cudaSuccess) return e;
   // no more CTAs than there can be units
-  const long long most = ((long long)a.N / kRows + a.B) * a.H;
+  const long long most = 2 * (((long long)a.N / kRows + a.B + 1) / 2) * a.H;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(most < a.sms ? most : a.sms));
+  cfg.gridDim = dim3((unsigned)(most < a.sms ? most : a.sms / 2 * 2));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
