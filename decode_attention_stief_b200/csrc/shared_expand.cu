@@ -13,9 +13,9 @@
 // order, heads innermost: a CTA keeps its rows in shared memory (two row tiles where they fit) and
 // streams the weights' 64-column chunks through a ring.
 //   warp 0: TMA producer; warp 1 of the first CTA: MMA issuer; warps 4-7 store the keys, warps 8-11
-//   the values, a thread a token: 32-byte stores, so that every store fills whole sectors (16-byte
-//   stores if an output is not 32-byte aligned).  The unit of head 0 also copies the position
-//   values.
+//   the values, through 4 KB of shared memory each, so that eight lanes store 128 neighbouring
+//   bytes of a token (stored by the thread that holds it, 32 bytes at a time, the weights' copies
+//   waited behind the stores).  The unit of head 0 also copies the position values.
 // Row tiles begin at multiples of 128 tokens of their sequence, hence at multiples of 64 rows of
 // a page: two copies bring 64 rows each.
 #include <cstdint>
@@ -31,6 +31,7 @@ namespace {
 constexpr int kRows = 128;                  // tokens a row tile
 constexpr uint32_t kAtomA = kRows * 128;    // 128 rows x 64 columns
 constexpr uint32_t kStageB = 128 * 128;     // 128 weight rows x 64 columns
+constexpr uint32_t kOutWarp = 32 * 128;     // an output warp's 32 tokens x 64 values
 constexpr int kThreads = 384;
 constexpr int kMaxStages = 6;
 constexpr uint32_t kTmemCols = 512;
@@ -40,16 +41,16 @@ struct Args {
   CUtensorMap mwk, mwv;  // W [H * 128][r], box 64 x 128
   SharedExpandArgs a;
   int chunks, na, nb;    // 64-column chunks of r, row tiles and weight chunks held
-  int wide;              // outputs are 32-byte aligned
 };
 
 struct Layout {
-  uint32_t b, bars, total;
+  uint32_t b, out, bars, total;
 };
 __host__ __device__ inline Layout layout_of(int chunks, int na, int nb) {
   Layout l;
   l.b = (uint32_t)(na * chunks) * kAtomA;
-  l.bars = l.b + (uint32_t)nb * kStageB;
+  l.out = l.b + (uint32_t)nb * kStageB;
+  l.bars = l.out + 8 * kOutWarp;
   l.total = l.bars + 8 * (2 * kMaxStages + 12);
   return l;
 }
@@ -116,17 +117,6 @@ struct Ring {
     }
   }
 };
-
-__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8], bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
-}
 
 }  // namespace
 
@@ -326,25 +316,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
       }
       if (!__all_sync(~0u, mbar_wait_bounded(&d_full[d], dp, a.dev_status))) break;
       tc_fence_after();
-      uint16_t* out = base + ((size_t)(u.s0 + t) * a.H + u.h) * 128;
       const uint32_t col = tmem + lanes + d * 256u + (uint32_t)half * 128u;
-#pragma unroll
+      uint8_t* stage = smem + lay.out + (uint32_t)(warp - 4) * kOutWarp;
+      const int row0 = u.j * kRows + quad * 32, piece = lane & 7;
+      uint16_t* out = base + ((size_t)(u.s0 + row0) * a.H + u.h) * 128 + piece * 8;
+#pragma unroll 1
       for (int c = 0; c < 128; c += 64) {
         uint32_t x[2][32];
         tmem_ld32(col + c, x[0]);
         tmem_ld32(col + c + 32, x[1]);
         tmem_wait_ld();
-        if (live) {
 #pragma unroll
-          for (int e = 0; e < 64; e += 16) {
-            uint32_t y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              y[i] = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 2 * i]),
-                                    __uint_as_float(x[e >> 5][(e & 31) + 2 * i + 1]));
-            store32(out + c + e, y, p.wide);
-          }
+        for (int e = 0; e < 64; e += 8) {  // a row's 16-byte pieces are rotated by its number
+          uint4 y;
+          y.x = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31)]), __uint_as_float(x[e >> 5][(e & 31) + 1]));
+          y.y = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 2]), __uint_as_float(x[e >> 5][(e & 31) + 3]));
+          y.z = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 4]), __uint_as_float(x[e >> 5][(e & 31) + 5]));
+          y.w = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 6]), __uint_as_float(x[e >> 5][(e & 31) + 7]));
+          *reinterpret_cast<uint4*>(stage + lane * 128 + (((e >> 3) ^ (lane & 7)) << 4)) = y;
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+          if (row0 + r < u.len) *reinterpret_cast<uint4*>(out + (size_t)r * a.H * 128 + c) = y;
+        }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -366,7 +364,6 @@ cudaError_t launch_shared_expand(const SharedExpandArgs& a, cudaStream_t stream)
   Args p{};
   p.a = a;
   p.chunks = (a.r + 63) / 64;
-  p.wide = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 31u) == 0;
   // two row tiles where at least three weight chunks fit beside them
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
   p.nb = 3;
