@@ -242,8 +242,10 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
         const uint64_t dp = sw128_desc(smem_u32(smem + lay.pe));
         const int pe_steps = a.dr / 16;
         int va = 0;
-        auto issue_s = [&](int i) -> bool {
-          if (!mbar_wait_bounded(&k_full[i % kKeySlots], (uint32_t)(i / kKeySlots & 1), a.dev_status)) return false;
+        auto wait_k = [&](int i) -> bool {
+          return mbar_wait_bounded(&k_full[i % kKeySlots], (uint32_t)(i / kKeySlots & 1), a.dev_status);
+        };
+        auto issue_s = [&](int i) {
           tc_fence_after();
           const uint64_t dk = sw128_desc(k_addr + (uint32_t)(i % kKeySlots) * kKeys);
 #pragma unroll
@@ -254,9 +256,9 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
             umma_bf16(s_col, dq + 2 * (kAtom >> 4) + 2 * kk, dp + 2 * kk, id_s, 1);
           umma_commit(&s_full[w]);
           umma_commit(&k_empty[i % kKeySlots]);
-          return true;
         };
-        bool ok = mbar_wait_bounded(&q_full[w], 0, a.dev_status) && issue_s(0);
+        bool ok = mbar_wait_bounded(&q_full[w], 0, a.dev_status) && wait_k(0);
+        if (ok) issue_s(0);
         for (int i = 0; ok && i < n; ++i) {
           const int vb = va + 1 == p.nv ? 0 : va + 1;
           if (!(ok = mbar_wait_bounded(&v_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status))) break;
@@ -264,6 +266,9 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
             mbar_arrive(partial);
             if (!(ok = mbar_wait_bounded(tail, 0, a.dev_status))) break;
           }
+          // (the next keys too are waited for while the softmax runs: a test of a barrier takes some
+          // 250 cycles next to the products' shared-memory traffic)
+          if (i + 1 < n && !(ok = wait_k(i + 1))) break;
           const uint64_t dva = sw128_mn_desc(v_addr + (uint32_t)va * kHalf, kHalf / 2);
           const uint64_t dvb = sw128_mn_desc(v_addr + (uint32_t)vb * kHalf, kHalf / 2);
           if (!(ok = mbar_wait_bounded(&p_half[w], (uint32_t)(i & 1), a.dev_status))) break;
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(o_col, s_col + 32 + kk * 8, dvb + kk * 128, id_o, 1);
           umma_commit(&v_empty[vb]);
-          if (i + 1 < n) ok = issue_s(i + 1);
+          if (i + 1 < n) issue_s(i + 1);
           else umma_commit(&o_full[w]);
           va = vb + 1 == p.nv ? 0 : vb + 1;
         }

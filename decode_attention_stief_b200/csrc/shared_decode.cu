@@ -632,11 +632,11 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
 // each, a CTA takes 128 dims of a head and its warps share the parts.  Bound by latency: the
 // lengths and the meta word are read together, then everything else of up to kBatch parts.
 template <int kWarps>
-__global__ void __launch_bounds__(256) stief_shared_merge_kernel(const SharedDecodeArgs a, int NH, int groups, int G) {
+__global__ void __launch_bounds__(kWarps == 1 ? 256 : 32 * kWarps) stief_shared_merge_kernel(const SharedDecodeArgs a, int NH, int groups, int G) {
   constexpr int kVec = kWarps == 1 ? 4 : 1;     // 128-dim chunks a warp holds
   constexpr int kBatch = kWarps == 1 ? 2 : 8;   // parts in flight
-  __shared__ float4 acc_s[8][32];
-  __shared__ float2 ml_s[8];
+  __shared__ float4 acc_s[kWarps][32];
+  __shared__ float2 ml_s[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
   const int nd = (a.r + 127) / 128;
   const int h = kWarps == 1 ? (int)blockIdx.x * 8 + warp : (int)blockIdx.x / nd;
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(256) stief_shared_merge_kernel(const SharedDec
   const int L = valid_length(__ldg(a.seq_lens + b), a.max_seq_len);
   const int2 meta = __ldcg(reinterpret_cast<const int2*>(ws + (size_t)b * 8));  // (garbage if L == 0)
   if (L > 0 && meta.y < 0) return;  // whole: written already
-  if (h >= a.Hq) return;            // (kWarps == 8: never, the grid is exact)
+  if (h >= a.Hq) return; // (kWarps > 1: never, the grid is exact)
   uint16_t* out = a.out + ((size_t)b * a.Hq + h) * a.r + d0;
   if (L == 0) {
     if (kWarps == 1 || warp == 0)
@@ -709,10 +709,10 @@ __global__ void __launch_bounds__(256) stief_shared_merge_kernel(const SharedDec
     if (lane == 0) ml_s[warp] = make_float2(M, l);
     __syncthreads();
     if (warp != 0) return;
-    for (int k = 1; k < 8; ++k) M = fmaxf(M, ml_s[k].x);
+    for (int k = 1; k < kWarps; ++k) M = fmaxf(M, ml_s[k].x);
     l = 0.f;
     acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kWarps; ++k) {
       const float f = fast_exp2(ml_s[k].x - M);
       const float4 o = acc_s[k][lane];
       l += f * ml_s[k].y;
@@ -796,8 +796,9 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   cfg.dynamicSmemBytes = 0;
   // many parts a sequence: a CTA's warps share them; else a warp a head
   if (p.G > 8 * a.B) {
+    cfg.blockDim = dim3(512);
     cfg.gridDim = dim3(a.Hq * p.nm, a.B);
-    return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<8>, a, p.NH, p.groups, p.G);
+    return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<16>, a, p.NH, p.groups, p.G);
   }
   cfg.gridDim = dim3((a.Hq + 7) / 8, a.B);
   return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<1>, a, p.NH, p.groups, p.G);
