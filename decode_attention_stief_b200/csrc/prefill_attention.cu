@@ -12,7 +12,7 @@
 //     O_w += P_w . V       (P in tensor memory, V MN-major as it lies in memory)
 // TMEM holds S_0, S_1, O_0, O_1, 128 columns each: all of it.  P_w overwrites S_w, whose row a
 // thread holds in registers meanwhile.  The tensor cores work for one tile of queries while the
-// softmax of the other runs; the product with the first 64 keys starts when half of P is there.
+// softmax of the other runs.
 //   warp 0: TMA producer; warps 1 and 3: MMA issuers of the two tiles; warp 2: zeroes the value
 //   rows past n_k in the last tile (they may hold NaN, and 0 * NaN is NaN); warps 4-7 and 8-11:
 //   softmax of the two tiles, one thread a query row, and the output.
@@ -99,6 +99,11 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
   constexpr uint32_t kTmemCols = kW * 256;   // S_w at 128 w, O_w at 128 (kW + w)
   constexpr uint32_t kOCol = kW * 128;
   constexpr int kKeySlots = kW;
+  // With one tile of queries the product with the first 64 keys starts when half of P is there (its
+  // memory is free, and the next values under way, that much sooner).  Two tiles that share the
+  // keys fall into step that way, and the tensor cores wait for both softmaxes at once: 8192
+  // tokens took 625 us with halves, 550 without.
+  constexpr bool kHalves = kW == 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t tmem_slot;
   const PrefillArgs& a = p.a;
@@ -258,6 +263,8 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
           umma_commit(&k_empty[i % kKeySlots]);
         };
         bool ok = mbar_wait_bounded(&q_full[w], 0, a.dev_status) && wait_k(0);
+        // (the second tile starts when the first has its weights: half a turn behind it)
+        if (kW == 2 && w == 1 && nt[0] > 0 && ok) ok = mbar_wait_bounded(&p_full[0], 0, a.dev_status);
         if (ok) issue_s(0);
         for (int i = 0; ok && i < n; ++i) {
           const int vb = va + 1 == p.nv ? 0 : va + 1;
@@ -266,23 +273,29 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
             mbar_arrive(partial);
             if (!(ok = mbar_wait_bounded(tail, 0, a.dev_status))) break;
           }
-          // (the next keys too are waited for while the softmax runs: a test of a barrier takes some
-          // 250 cycles next to the products' shared-memory traffic)
-          if (i + 1 < n && !(ok = wait_k(i + 1))) break;
+          // With a CTA to itself a tile of queries waits for its next keys while the softmax runs: a
+          // test of a barrier takes some 250 cycles next to the products' shared-memory traffic.
+          // Two tiles that share keys do it later: the next position part comes only when both have
+          // their products with this one.
+          if (kW == 1 && i + 1 < n && !(ok = wait_k(i + 1))) break;
           const uint64_t dva = sw128_mn_desc(v_addr + (uint32_t)va * kHalf, kHalf / 2);
           const uint64_t dvb = sw128_mn_desc(v_addr + (uint32_t)vb * kHalf, kHalf / 2);
-          if (!(ok = mbar_wait_bounded(&p_half[w], (uint32_t)(i & 1), a.dev_status))) break;
+          if (!(ok = mbar_wait_bounded(kHalves ? &p_half[w] : &p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(o_col, s_col + kk * 8, dva + kk * 128, id_o, i > 0 || kk > 0);
           umma_commit(&v_empty[va]);
-          if (!(ok = mbar_wait_bounded(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
+          if (kHalves && !(ok = mbar_wait_bounded(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(o_col, s_col + 32 + kk * 8, dvb + kk * 128, id_o, 1);
           umma_commit(&v_empty[vb]);
-          if (i + 1 < n) issue_s(i + 1);
-          else umma_commit(&o_full[w]);
+          if (i + 1 < n) {
+            if (kW == 2 && !(ok = wait_k(i + 1))) break;
+            issue_s(i + 1);
+          } else {
+            umma_commit(&o_full[w]);
+          }
           va = vb + 1 == p.nv ? 0 : vb + 1;
         }
         // products left by a timeout get a bounded chance to finish; on the normal path this is
@@ -385,7 +398,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
           w16[e] = pack_bf16x2_rn(lo, hi);
         }
         tmem_st16(s_col + 16 * c, w16);
-        if (c == 1) {
+        if (kHalves && c == 1) {
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
