@@ -51,6 +51,9 @@ struct Args {
   int qtiles;       // tiles of 256 queries of the longest sequence
   float scale2;     // |scale| * log2(e)
   int negate;       // scale < 0: the products are negated instead
+#ifdef STIEF_TEST_HOOKS
+  uint32_t stall;     // test build: bytes expected of the first copy that none delivers
+#endif
 };
 
 // Queries (kW tiles), key slots, one slot of position parts, slots of 64 value rows.  A key tile's
@@ -122,6 +125,11 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
   uint64_t* tail = q_full + 11;             // its rows past n_k are cleared
   uint64_t* drain = q_full + 12;            // [2]
 
+#ifdef STIEF_TEST_HOOKS
+  const uint32_t stall = p.stall;
+#else
+  constexpr uint32_t stall = 0u;
+#endif
   if ((smem_u32(smem) & 1023u) != 0) {
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
     return;
@@ -193,7 +201,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
         int nkl = 0, nvl = 0;  // key tiles and value halves requested
         const bool half[2] = {nt[0] > 0, nt[1] > 0}, pos = p.atoms > 2;
         auto load_q = [&](int w) {
-          mbar_arrive_expect_tx(&q_full[w], (uint32_t)p.atoms * kAtom);
+          mbar_arrive_expect_tx(&q_full[w], (uint32_t)p.atoms * kAtom + stall);
           for (int c = 0; c < p.atoms; ++c)
             tma_load_2d(smem + (uint32_t)(w * p.atoms + c) * kAtom, &p.mq, h * dq + 64 * c, q0 + first + w * kRows,
                         &q_full[w], once);
@@ -470,6 +478,9 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
   p.scale2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
   if (p.scale2 < 1e-30f) p.scale2 = 1e-30f;  // above 0, so that a masked score stays -inf
   p.negate = a.scale < 0;
+#ifdef STIEF_TEST_HOOKS
+  p.stall = test_stall_bytes();
+#endif
   const long long blocks = (long long)p.qtiles * a.Hq * a.B;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const uint32_t smem = layout_of<kW>(p.atoms, p.nv).total;

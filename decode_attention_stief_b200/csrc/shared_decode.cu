@@ -67,6 +67,9 @@ struct Args {
   int whole_rows;     // w % 64 == 0: one copy brings a tile's atoms
   int whole;          // sequences are not split over CTAs, and there is no second kernel
   float scale2;       // scale * log2(e)
+#ifdef STIEF_TEST_HOOKS
+  uint32_t stall;     // test build: bytes expected of the first copy that none delivers
+#endif
 };
 
 struct Layout {
@@ -183,6 +186,11 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   uint64_t* tail = q_full + 12;          // its rows past the length are cleared
   volatile uint32_t* stop = reinterpret_cast<uint32_t*>(q_full + 13);  // the first issuer gave up
 
+#ifdef STIEF_TEST_HOOKS
+  const uint32_t stall = p.stall;
+#else
+  constexpr uint32_t stall = 0u;
+#endif
   if ((smem_u32(smem) & 1023u) != 0) {  // swizzled operands need 1 KiB alignment
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
     return;
@@ -285,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       while (ok && walk.next(seg)) {
         if (segs > 0) ok = mbar_wait_bounded(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status);
         if (!ok) break;
-        mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128));
+        mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128) + (segs == 0 ? stall : 0u));
         for (int c = 0; c < p.na; ++c)
           tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, seg.b * a.Hq + h_base, q_full, keep);
         ++segs;
@@ -746,6 +754,9 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   const int ctas = a.sms < kMaxCtas ? a.sms : kMaxCtas;
   p.G = ctas / p.groups;
   p.scale2 = a.scale * 1.4426950408889634f;
+#ifdef STIEF_TEST_HOOKS
+  p.stall = test_stall_bytes();
+#endif
   // Short sequences are finished by one CTA each: the second kernel costs 2 us, as much as two
   // further tiles.  (5 sequences of up to 200 tokens: 7.9 us with it.)
   p.whole = a.max_seq_len <= kWholeTiles * kTok;

@@ -41,6 +41,9 @@ struct Args {
   CUtensorMap mwk, mwv;  // W [H * 128][r], box 64 x 128
   SharedExpandArgs a;
   int chunks, na, nb;    // 64-column chunks of r, row tiles and weight chunks held
+#ifdef STIEF_TEST_HOOKS
+  uint32_t stall;     // test build: bytes expected of the first copy that none delivers
+#endif
 };
 
 struct Layout {
@@ -138,6 +141,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
   uint64_t* d_empty = a_full + 6;           // [2] it has been read
   uint64_t* drain = a_full + 8;
 
+#ifdef STIEF_TEST_HOOKS
+  const uint32_t stall = p.stall;
+#else
+  constexpr uint32_t stall = 0u;
+#endif
   if ((smem_u32(smem) & 1023u) != 0) {  // (the same in both CTAs)
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
     return;
@@ -226,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
         if (u.new_tile) {
           if (na >= p.na && !(ok = mbar_wait_bounded(&a_empty[ra.st], ra.ph ^ 1u, a.dev_status))) break;
           const uint32_t bar = in_cta(&a_full[ra.st], 0);
-          if (leader) mbar_arrive_expect_tx(&a_full[ra.st], 2u * p.chunks * kAtomA);
+          if (leader) mbar_arrive_expect_tx(&a_full[ra.st], 2u * p.chunks * kAtomA + (na == 0 ? stall : 0u));
           uint8_t* dst = smem + (uint32_t)(ra.st * p.chunks) * kAtomA;
           for (int half = 0; half < 2; ++half) {
             const int pos = u.j * kRows + half * 64, pi = pos / a.page_size;
@@ -364,6 +372,9 @@ cudaError_t launch_shared_expand(const SharedExpandArgs& a, cudaStream_t stream)
   Args p{};
   p.a = a;
   p.chunks = (a.r + 63) / 64;
+#ifdef STIEF_TEST_HOOKS
+  p.stall = test_stall_bytes();
+#endif
   // two row tiles where at least three weight chunks fit beside them
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
   p.nb = 3;
