@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(kPlanThreads) stief_page_plan_kernel(const Pla
   int* need = upto + B;       // [B] new pages (0 when refused)
   int* tail = need + B;       // [B] page of token L_b when it is already held, else -1
   int* lead = tail + B;       // [B] first new page
+  // Of several CTAs the last one writes everything but the slots, which the others share.
+  const bool alone = gridDim.x == 1, clerk = blockIdx.x == gridDim.x - 1;
   const int per = (B + nthreads - 1) / nthreads, b0 = tid * per, b1 = min(B, b0 + per);  // per <= kPer
   if (tid == 0) used_s = 0;
 
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) stief_page_plan_kernel(const Pla
         } else {
           used = (int)p;
           // the first new page, which is all that most steps need
-          if (blockIdx.x == 0) {
+          if (clerk) {
             const int id = a.free_pages[n - 1 - upto[b]];
             lead[b] = id;  // (kept by the only CTA of a small step)
             a.block_table[(size_t)b * a.max_pages + first[b]] = id;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) stief_page_plan_kernel(const Pla
       const int b = b0 + k;
       if (need[b] > 1) work |= 1u;
       if (T[k] > kDirect) work |= 2u;
-      if (a.slots && gridDim.x == 1 && T[k] > 0 && T[k] <= kDirect) {
+      if (a.slots && alone && T[k] > 0 && T[k] <= kDirect) {
         const int held = first[b] * ps;  // tokens up to here are in pages held before
         for (int i = 0; i < T[k]; ++i) {
           const int t = L[k] + i, pg = t < held ? tail[b] : lead[b];
@@ -184,14 +186,14 @@ __global__ void __launch_bounds__(kPlanThreads) stief_page_plan_kernel(const Pla
     }
   // This CTA has read the lengths and the free count: the last one to have done so may write them.
   const bool more_pages = __syncthreads_or((int)(work & 1u)) != 0, more_tokens = __syncthreads_or((int)(work & 2u)) != 0;
-  if (gridDim.x > 1) {
+  if (!alone) {
     if (tid == 0) {
       __threadfence();
       last_s = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
   }
-  if (gridDim.x == 1 || last_s) {
+  if (alone || last_s) {
     if (a.seq_lens_out) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
@@ -199,10 +201,10 @@ __global__ void __launch_bounds__(kPlanThreads) stief_page_plan_kernel(const Pla
     }
     if (tid == 0) {
       *a.free_count_out = n - used_s;
-      if (gridDim.x > 1) *a.ticket = 0u;
+      if (!alone) *a.ticket = 0u;
     }
   }
-  if (blockIdx.x == 0) {
+  if (clerk) {
     if (bits) report(a.dev_status, bits);
     if (a.q_start) {
       for (int b = b0; b < b1; ++b) a.q_start[b] = qs[b];
@@ -235,14 +237,15 @@ __global__ void __launch_bounds__(kPlanThreads) stief_page_plan_kernel(const Pla
 
   // slots: the CTA's share of the flat tokens
   if (!a.slots) return;
-  if (gridDim.x == 1 && !more_tokens) {
+  if (alone && !more_tokens) {
     for (long long i = total_tokens + tid; i < a.max_tokens; i += nthreads) a.slots[i] = -1;
     return;
   }
   // (one bisection and one division for four tokens; 16-byte stores if the array allows them)
   const bool wide = (reinterpret_cast<uintptr_t>(a.slots) & 15u) == 0;
-  for (long long i0 = 4LL * ((long long)blockIdx.x * nthreads + tid); i0 < a.max_tokens;
-       i0 += 4LL * nthreads * gridDim.x) {
+  if (!alone && clerk) return;
+  const long long writers = alone ? 1 : gridDim.x - 1;
+  for (long long i0 = 4LL * ((long long)blockIdx.x * nthreads + tid); i0 < a.max_tokens; i0 += 4LL * nthreads * writers) {
     int s[4] = {-1, -1, -1, -1};
     if (i0 < total_tokens) {
       int b = upper_index(qs, B, (int)i0), page = -1, at = ps;  // at: offset in the page, ps: look up
@@ -288,7 +291,8 @@ cudaError_t launch_page_plan(const PlanArgs& a, int sms, cudaStream_t stream) {
   const int threads = a.B <= 256 && a.max_tokens <= 1024 ? 256 : a.B <= 512 * kPer ? 512 : kPlanThreads;
   long long grid = a.slots ? (a.max_tokens + 4LL * threads - 1) / (4 * threads) : 1;
   if (grid < 1) grid = 1;
-  if (grid > 2 * sms) grid = 2 * sms;
+  if (grid > 2 * sms - 1) grid = 2 * sms - 1;
+  if (grid > 1) ++grid;  // the one that writes the rest
   const int smem = 7 * 4 * a.B;
   static SmemLimit limit;
   cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_page_plan_kernel), a.device, smem);

@@ -207,6 +207,8 @@ stief_status stief_prefill_attention(const uint16_t* q, const uint16_t* k, const
       dr % 16 != 0 || Nq < 0 || Nkv < 0 || max_q_len < 0 || !std::isfinite(scale))
     return STIEF_ERR_INVALID_ARG;
   if (Nq == 0 || max_q_len == 0) return STIEF_OK;
+  const long long tiles = ((max_q_len < Nq ? max_q_len : Nq) + 127LL) / 128;
+  if (tiles * Hq * B >= (1LL << 31)) return STIEF_ERR_INVALID_ARG;  // one block each
   if (!q || !q_start || !kv_start || !out || (Nkv > 0 && (!k || !v || (dr > 0 && !k_pe))))
     return STIEF_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_pe) || !aligned16(out) ||

@@ -348,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
         for (int i = 0; i < 8; ++i) {
           const int r = 4 * i + (lane >> 3);
           const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
-          if (row0 + r < u.len) *reinterpret_cast<uint4*>(out + (size_t)r * a.H * 128 + c) = y;
+          if (row0 + r < u.len) __stcs(reinterpret_cast<uint4*>(out + (size_t)r * a.H * 128 + c), y);
         }
         __syncwarp();
       }

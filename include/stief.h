@@ -591,7 +591,7 @@ STIEF_API stief_status stief_plan_pages(const int32_t* new_tokens, const int32_t
  *   pe_new : bf16, row i at pe_new + i * pe_stride, >= dr (NULL if dr == 0)
  *   slots  : int32 [N]; a negative slot skips its row, one past the pool too, with
  *            STIEF_DEV_CAPACITY_OVERFLOW.  Slots must be distinct: the row of a slot given
- *            twice is a mixture.
+ *            twice is a mixture.  The pool must not overlap the inputs.
  */
 STIEF_API stief_status stief_append_shared_paged(const uint16_t* c_new, const uint16_t* pe_new,
                               const int32_t* slots, uint16_t* pages, int N, int r, int dr,
@@ -650,7 +650,8 @@ STIEF_API stief_status stief_expand_shared_paged(const uint16_t* pages, const in
  * q_start, kv_start : int32 [B + 1].  A sequence whose rows are not within [0, Nq) and
  * [0, Nkv), or with more than max_q_len queries, is skipped with STIEF_DEV_BAD_LENGTH.  Output
  * rows of no sequence are left as they were.  d == 128, 0 <= dr <= 64 a multiple of 16,
- * Hq <= 256.  The weights enter the second product rounded to bf16.  Rows of no sequence, or of
+ * Hq <= 256, B * Hq * ceil(max_q_len / 128) < 2^31.  The weights enter the second product rounded
+ * to bf16.  Rows of no sequence, or of
  * another one, may hold anything; a value row of the sequence itself that is not finite may also
  * reach queries of the same sequence that do not see it (as a weight of 0).
  */

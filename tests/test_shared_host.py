@@ -61,6 +61,7 @@ DECODE = dict(q=FAKE, pages=FAKE, table=FAKE, lens=FAKE, out=FAKE, ws=FAKE, ws_b
     (dict(out=None), INVALID), (dict(B=0), INVALID), (dict(B=65536), INVALID), (dict(Hq=0), INVALID), (dict(Hq=257), INVALID),
     (dict(r=8), INVALID), (dict(dr=72), INVALID), (dict(page_size=96), INVALID), (dict(num_pages=0), INVALID),
     (dict(most=-1), INVALID), (dict(most=257), CAPACITY), (dict(scale=float("nan")), INVALID),
+    (dict(B=65535, max_pages=1 << 24, most=1 << 30), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(q=FAKE + 8), ALIGN), (dict(pages=FAKE + 2), ALIGN),
     (dict(out=FAKE + 4), ALIGN), (dict(table=FAKE + 2), ALIGN), (dict(lens=FAKE + 1), ALIGN), (dict(ws=FAKE + 8), ALIGN),
     (dict(ws=None), WORKSPACE), (dict(ws_bytes=16), WORKSPACE),
@@ -95,6 +96,7 @@ PREFILL = dict(q=FAKE, k=FAKE, v=FAKE, pe=FAKE, qs=FAKE, ks=FAKE, out=FAKE, B=2,
     (dict(dr=24), INVALID), (dict(Nq=-1), INVALID), (dict(Nkv=-1), INVALID), (dict(most=-1), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(q=FAKE + 8), ALIGN), (dict(v=FAKE + 2), ALIGN), (dict(pe=FAKE + 4), ALIGN),
     (dict(out=FAKE + 2), ALIGN), (dict(qs=FAKE + 2), ALIGN), (dict(Nq=0, q=None), OK), (dict(most=0), OK),
+    (dict(B=65535, Hq=256, Hkv=256, Nq=1 << 20, most=1 << 20), INVALID),
 ])
 def test_prefill_argument_errors(lib, kw, code):
     assert _call(lib.stief_prefill_attention, list(PREFILL), PREFILL, kw) == code
