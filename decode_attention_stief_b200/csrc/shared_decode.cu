@@ -21,10 +21,11 @@
 //   the length in a sequence's last tile (they may hold NaN, and 0 * NaN is NaN); warps 4-7:
 //   softmax, rescaling and the output.  S has two buffers, so the tensor cores work on the next
 //   tile during a tile's softmax.
-// The running maximum is a reference that only moves when a score passes it by more than 2^8:
-// the accumulator is then rescaled in TMEM (rare); weights are at most 2^8 and rounded to bf16
-// once, and the sum l adds the rounded weights, so that a weight's rounding cancels where it
-// dominates.
+// The softmax's reference is the first tile's maximum of the head and moves only when a score
+// passes it by more than 2^60 (rare: the accumulator is then rescaled in TMEM).  Weights and sums
+// are floating-point numbers, so a large weight loses nothing, and the maximum of a tile, needed
+// only for that test, is off the path from S to P.  Weights are rounded to bf16 once, and the sum
+// l adds the rounded weights, so that a weight's rounding cancels where it dominates.
 //
 // Work: the 64-token tiles of all sequences, in order, are dealt out evenly: CTA c takes tiles
 // [c per, (c + 1) per), so ragged batches and single long sequences fill the GPU alike.  A
@@ -53,7 +54,7 @@ constexpr int kMaxCtas = 160;       // the workspace holds two partial states fo
 constexpr int kMinTiles = 2;        // tiles per CTA at least (fewer would only add merging)
 constexpr uint32_t kSCol = 256;     // TMEM: O~^T at 0, S buffers at 256 and 320
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescale = 8.f;     // log2 units the reference may lag behind
+constexpr float kRescale = 60.f;    // log2 units a score may pass the reference by
 
 struct Args {
   CUtensorMap mq;     // q [B * Hq][w], box 64 x heads
@@ -66,7 +67,8 @@ struct Args {
   int nstage;
   int whole_rows;     // w % 64 == 0: one copy brings a tile's atoms
   int whole;          // sequences are not split over CTAs, and there is no second kernel
-  float scale2;       // scale * log2(e)
+  float scale2;       // |scale| * log2(e)
+  int negate;         // scale < 0: the products are negated instead
 #ifdef STIEF_TEST_HOOKS
   uint32_t stall;     // test build: bytes expected of the first copy that none delivers
 #endif
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     // test, shuffle or vote between them costs 100 cycles and more.  The two products have a
     // thread each, so that neither waits for what the other one lacks.)
     if (elect_one()) {
-      const uint32_t id_s = idesc_bf16_f32(64, kTok, false, false);
+      const uint32_t id_s = idesc_bf16_f32(64, kTok, false, false) | (p.negate ? 1u << 13 : 0u);  // (bit 13: -q~)
       const uint32_t stage0 = smem_u32(smem + lay.stages), stage_bytes = (uint32_t)p.sa * kAtom;
       const uint32_t q_step = (uint32_t)(p.NH * 128) >> 4;
       const int whole0 = min(p.n0, p.w / 64), whole1 = p.w / 64 - whole0, steps_left = p.w % 64 / 16;
@@ -461,78 +463,95 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     while (walk.next(seg)) {
       float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
       for (int t = seg.t0; t < seg.t1; ++t, ++i) {
-        float x[kTok / 2];
-        float f0 = 1.f, f1 = 1.f;
-        bool move = false;
-        if (active) {
-          bad |= !mbar_wait_bounded(&s_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status);
-          tc_fence_after();
-          uint32_t v[kTok / 2];
-          tmem_ld_16x256b(tmem + lane_addr + kSCol + (uint32_t)(i & 1) * kTok, v);
-          tmem_wait_ld();
-          const int valid = seg.L - t * kTok;
-          float t0 = -INFINITY, t1 = -INFINITY;
+        uint32_t v[kTok / 2], w[kTok / 4];
+        float f0 = 1.f, f1 = 1.f, t0 = -1e30f, t1 = -1e30f, a0 = 0.f, a1 = 0.f;
+        // weights with the references m0, m1, and their sums (of the rounded weights)
+        auto weights = [&]() {
+          const uint64_t sc = pack2(p.scale2, p.scale2), n0 = pack2(-m0, -m0), n1 = pack2(-m1, -m1);
+          a0 = a1 = 0.f;
 #pragma unroll
-          for (int j = 0; j < kTok / 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool in = 8 * j + col + e < valid;
-              x[4 * j + e] = in ? __uint_as_float(v[4 * j + e]) * p.scale2 : -INFINITY;
-              x[4 * j + 2 + e] = in ? __uint_as_float(v[4 * j + 2 + e]) * p.scale2 : -INFINITY;
-              t0 = fmaxf(t0, x[4 * j + e]);
-              t1 = fmaxf(t1, x[4 * j + 2 + e]);
-            }
+          for (int j = 0; j < kTok / 8; ++j) {
+            const uint64_t x0 = fma2(((uint64_t)v[4 * j + 1] << 32) | v[4 * j], sc, n0);
+            const uint64_t x1 = fma2(((uint64_t)v[4 * j + 3] << 32) | v[4 * j + 2], sc, n1);
+            w[2 * j] = pack_bf16x2_rn(fast_exp2(lo_of(x0)), fast_exp2(hi_of(x0)));
+            w[2 * j + 1] = pack_bf16x2_rn(fast_exp2(lo_of(x1)), fast_exp2(hi_of(x1)));
+            a0 += bf16lo(w[2 * j]) + bf16hi(w[2 * j]);
+            a1 += bf16lo(w[2 * j + 1]) + bf16hi(w[2 * j + 1]);
+          }
+        };
+        auto over_lanes = [&]() {  // maxima of the four lanes that share a head
           t0 = fmaxf(t0, __shfl_xor_sync(~0u, t0, 1));
           t1 = fmaxf(t1, __shfl_xor_sync(~0u, t1, 1));
           t0 = fmaxf(t0, __shfl_xor_sync(~0u, t0, 2));
           t1 = fmaxf(t1, __shfl_xor_sync(~0u, t1, 2));
-          if (t == seg.t0) {  // (a floor, so that a tile of -inf scores weighs 0 and not NaN)
-            m0 = fmaxf(t0, -1e30f);
-            m1 = fmaxf(t1, -1e30f);
-          } else {
+        };
+        bool move = false;
+        if (active) {
+          bad |= !mbar_wait_bounded(&s_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status);
+          tc_fence_after();
+          tmem_ld_16x256b(tmem + lane_addr + kSCol + (uint32_t)(i & 1) * kTok, v);
+          tmem_wait_ld();
+          const int valid = seg.L - t * kTok;
+          if (valid < kTok) {
+#pragma unroll
+            for (int j = 0; j < kTok / 8; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (8 * j + col + e >= valid) v[4 * j + e] = v[4 * j + 2 + e] = 0xff800000u;  // -inf
+          }
+          float s0 = -INFINITY, s1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < kTok / 8; ++j) {
+            s0 = max3(s0, __uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]));
+            s1 = max3(s1, __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+          }
+          // (a floor, so that a tile of -inf scores weighs 0 and not NaN)
+          t0 = fmaxf(s0 * p.scale2, -1e30f);
+          t1 = fmaxf(s1 * p.scale2, -1e30f);
+          if (t == seg.t0) {  // the reference: the first tile's maximum
+            over_lanes();
+            m0 = t0;
+            m1 = t1;
+          }
+          weights();
+          move = (t0 > m0 + kRescale && r0 < nheads) || (t1 > m1 + kRescale && r0 + 8 < nheads);
+        }
+        if (named_bar_or(1, 128, move || bad)) {
+          if (named_bar_or(1, 128, bad)) break;
+          // some head's reference moves: weigh the tile again and scale its column of O~^T, once the
+          // last product is in
+          if (active) {
+            over_lanes();
             if (t0 > m0 + kRescale) {
               f0 = fast_exp2(m0 - t0);
               m0 = t0;
-              move |= r0 < nheads;
             }
             if (t1 > m1 + kRescale) {
               f1 = fast_exp2(m1 - t1);
               m1 = t1;
-              move |= r0 + 8 < nheads;
             }
-          }
-        }
-        if (named_bar_or(1, 128, move || bad)) {
-          if (named_bar_or(1, 128, bad)) break;
-          // some head's reference moved: scale its column of O~^T, once the last product is in
-          if (active && (lane & 3) == 0) {
-            sm_f[r0] = f0;
-            sm_f[r0 + 8] = f1;
+            weights();
+            if ((lane & 3) == 0) {
+              sm_f[r0] = f0;
+              sm_f[r0 + 8] = f1;
+            }
           }
           bad |= !mbar_wait_bounded(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
           if (named_bar_or(1, 128, bad)) break;
           tc_fence_after();
           for (int c = 0; c < p.nm * p.NH; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(tmem + lane_addr + (uint32_t)c, v);
+            uint32_t o[16];
+            tmem_ld16(tmem + lane_addr + (uint32_t)c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * lds_f32(smem_u32(sm_f + c % p.NH + e)));
-            tmem_st16(tmem + lane_addr + (uint32_t)c, v);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * lds_f32(smem_u32(sm_f + c % p.NH + e)));
+            tmem_st16(tmem + lane_addr + (uint32_t)c, o);
           }
           tmem_wait_st();
         }
-        l0 *= f0;
-        l1 *= f1;
+        l0 = l0 * f0 + a0;
+        l1 = l1 * f1 + a1;
         if (active) {
-          uint32_t w[kTok / 4];
-#pragma unroll
-          for (int j = 0; j < kTok / 8; ++j) {
-            w[2 * j] = pack_bf16x2_rn(fast_exp2(x[4 * j] - m0), fast_exp2(x[4 * j + 1] - m0));
-            w[2 * j + 1] = pack_bf16x2_rn(fast_exp2(x[4 * j + 2] - m1), fast_exp2(x[4 * j + 3] - m1));
-            l0 += bf16lo(w[2 * j]) + bf16hi(w[2 * j]);
-            l1 += bf16lo(w[2 * j + 1]) + bf16hi(w[2 * j + 1]);
-          }
           // P's buffer is free once the last tile's product is in
           if (i >= 1 && !mbar_wait_bounded(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status))
             bad = true;
@@ -753,7 +772,9 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   p.groups = (a.Hq + p.NH - 1) / p.NH;
   const int ctas = a.sms < kMaxCtas ? a.sms : kMaxCtas;
   p.G = ctas / p.groups;
-  p.scale2 = a.scale * 1.4426950408889634f;
+  p.scale2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
+  if (p.scale2 < 1e-30f) p.scale2 = 1e-30f;  // above 0, so that a masked score stays -inf
+  p.negate = a.scale < 0;
 #ifdef STIEF_TEST_HOOKS
   p.stall = test_stall_bytes();
 #endif
