@@ -191,18 +191,18 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
         for (int i = 0; ok && i < tiles; ++i) {
           const int row = k0 + i * kRows, ks = i % kKeySlots;
           if (i == 0 && half[0]) load_q(0);
-          if (i >= kKeySlots && !(ok = mbar_wait_bounded(&k_empty[ks], (uint32_t)(i / kKeySlots & 1) ^ 1u, a.dev_status))) break;
+          if (i >= kKeySlots && !(ok = mbar_wait_ready(&k_empty[ks], (uint32_t)(i / kKeySlots & 1) ^ 1u, a.dev_status))) break;
           mbar_arrive_expect_tx(&k_full[ks], kKeys + (pos ? kAtom : 0u));
           tma_load_3d(smem + lay.k + (uint32_t)ks * kKeys, &p.mk, 0, row, hk * 2, &k_full[ks], keep);
           ++nkl;
           if (pos) {  // (its one slot is free when the last tile's keys are)
-            if (i > 0) ok = mbar_wait_bounded(&k_empty[(i - 1) % kKeySlots], (uint32_t)((i - 1) / kKeySlots & 1), a.dev_status);
+            if (i > 0) ok = mbar_wait_ready(&k_empty[(i - 1) % kKeySlots], (uint32_t)((i - 1) / kKeySlots & 1), a.dev_status);
             tma_load_2d(smem + lay.pe, &p.mp, 0, row, &k_full[ks], keep);  // (after a timeout too: it is expected)
             if (!ok) break;
           }
           if (i == 0 && half[1]) load_q(1);
           for (int c = 0; c < 2; ++c) {
-            if (nvl >= p.nv && ok) ok = mbar_wait_bounded(&v_empty[vs], vp ^ 1u, a.dev_status);
+            if (nvl >= p.nv && ok) ok = mbar_wait_ready(&v_empty[vs], vp ^ 1u, a.dev_status);
             if (!ok && c == 0) break;
             if (c == 0) mbar_arrive_expect_tx(&v_full[i & 1], 2 * kHalf);
             tma_load_3d(smem + lay.v + (uint32_t)vs * kHalf, &p.mv, 0, row + 64 * c, hk * 2, &v_full[i & 1], keep);
@@ -213,11 +213,11 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
         // every requested copy lands before the shared memory is released
         if (tiles > 0) {
           for (int w = 0; w < 2; ++w)
-            if (half[w]) mbar_wait_bounded(&q_full[w], 0, nullptr);
+            if (half[w]) mbar_wait_ready(&q_full[w], 0, nullptr);
           for (int j = max(0, nkl - kKeySlots); j < nkl; ++j)
-            mbar_wait_bounded(&k_full[j % kKeySlots], (uint32_t)(j / kKeySlots & 1), nullptr);
+            mbar_wait_ready(&k_full[j % kKeySlots], (uint32_t)(j / kKeySlots & 1), nullptr);
           for (int j = max(0, nvl / 2 - 2); j < nvl / 2; ++j)
-            mbar_wait_bounded(&v_full[j & 1], (uint32_t)((j >> 1) & 1), nullptr);
+            mbar_wait_ready(&v_full[j & 1], (uint32_t)((j >> 1) & 1), nullptr);
         }
       }
     } else if (warp == 1 || (kW == 2 && warp == 3)) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
         const int pe_steps = a.dr / 16;
         int va = 0;
         auto wait_k = [&](int i) -> bool {
-          return mbar_wait_bounded(&k_full[i % kKeySlots], (uint32_t)(i / kKeySlots & 1), a.dev_status);
+          return mbar_wait_ready(&k_full[i % kKeySlots], (uint32_t)(i / kKeySlots & 1), a.dev_status);
         };
         auto issue_s = [&](int i) {
           tc_fence_after();
@@ -249,16 +249,16 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
           umma_commit(&s_full[w]);
           umma_commit(&k_empty[i % kKeySlots]);
         };
-        bool ok = mbar_wait_bounded(&q_full[w], 0, a.dev_status) && wait_k(0);
+        bool ok = mbar_wait_ready(&q_full[w], 0, a.dev_status) && wait_k(0);
         // (the second tile starts when the first has its weights: half a turn behind it)
-        if (kW == 2 && w == 1 && nt[0] > 0 && ok) ok = mbar_wait_bounded(&p_full[0], 0, a.dev_status);
+        if (kW == 2 && w == 1 && nt[0] > 0 && ok) ok = mbar_wait_ready(&p_full[0], 0, a.dev_status);
         if (ok) issue_s(0);
         for (int i = 0; ok && i < n; ++i) {
           const int vb = va + 1 == p.nv ? 0 : va + 1;
-          if (!(ok = mbar_wait_bounded(&v_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status))) break;
+          if (!(ok = mbar_wait_ready(&v_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status))) break;
           if (i == tiles - 1 && (i + 1) * kRows > n_k) {  // rows past n_k must not be NaN
             mbar_arrive(partial);
-            if (!(ok = mbar_wait_bounded(tail, 0, a.dev_status))) break;
+            if (!(ok = mbar_wait_ready(tail, 0, a.dev_status))) break;
           }
           // With a CTA to itself a tile of queries waits for its next keys while the softmax runs: a
           // test of a barrier takes some 250 cycles next to the products' shared-memory traffic.
@@ -267,12 +267,12 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
           if (kW == 1 && i + 1 < n && !(ok = wait_k(i + 1))) break;
           const uint64_t dva = sw128_mn_desc(v_addr + (uint32_t)va * kHalf, kHalf / 2);
           const uint64_t dvb = sw128_mn_desc(v_addr + (uint32_t)vb * kHalf, kHalf / 2);
-          if (!(ok = mbar_wait_bounded(kHalves ? &p_half[w] : &p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
+          if (!(ok = mbar_wait_ready(kHalves ? &p_half[w] : &p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(o_col, s_col + kk * 8, dva + kk * 128, id_o, i > 0 || kk > 0);
           umma_commit(&v_empty[va]);
-          if (kHalves && !(ok = mbar_wait_bounded(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
+          if (kHalves && !(ok = mbar_wait_ready(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(o_col, s_col + 32 + kk * 8, dvb + kk * 128, id_o, 1);
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
         // products left by a timeout get a bounded chance to finish; on the normal path this is
         // the end of the last one
         umma_commit(&drain[w]);
-        mbar_wait_bounded(&drain[w], 0, nullptr);
+        mbar_wait_ready(&drain[w], 0, nullptr);
       }
     } else if (warp == 2) {
       // -------------------------------------------------------------- value rows past n_k
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
     uint64_t l0 = 0, l1 = 0;
     bool ok = true;
     for (int i = 0; i < nt[w]; ++i) {
-      ok = __all_sync(~0u, mbar_wait_bounded(&s_full[w], (uint32_t)(i & 1), a.dev_status));
+      ok = __all_sync(~0u, mbar_wait_ready(&s_full[w], (uint32_t)(i & 1), a.dev_status));
       if (!ok) break;
       tc_fence_after();
       uint32_t s[4][32];
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
       if (lane == 0) mbar_arrive(&p_full[w]);
     }
     // the output: zeros for a row that sees no key
-    if (ok && nt[w] > 0) ok = __all_sync(~0u, mbar_wait_bounded(&o_full[w], 0, a.dev_status));
+    if (ok && nt[w] > 0) ok = __all_sync(~0u, mbar_wait_ready(&o_full[w], 0, a.dev_status));
     if (ok) {
       tc_fence_after();
       const uint64_t ls = add2(l0, l1);

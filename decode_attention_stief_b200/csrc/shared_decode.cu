@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       Ring ring{p.nstage};
       bool ok = true;
       while (ok && walk.next(seg)) {
-        if (segs > 0) ok = mbar_wait_bounded(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status);
+        if (segs > 0) ok = mbar_wait_ready(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status);
         if (!ok) break;
         mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128) + (segs == 0 ? stall : 0u));
         for (int c = 0; c < p.na; ++c)
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
           uint8_t* dst = smem + lay.stages + (uint32_t)(st * p.sa) * kAtom;
           for (int piece = 0; piece < pieces; ++piece) {
             uint64_t* bar = &full[2 * st + piece];
-            if (i >= p.nstage && !(ok = mbar_wait_bounded(&empty[2 * st + piece], ring.ph ^ 1u, a.dev_status))) break;
+            if (i >= p.nstage && !(ok = mbar_wait_ready(&empty[2 * st + piece], ring.ph ^ 1u, a.dev_status))) break;
             const int c0 = piece ? p.n0 : 0, c1 = piece ? p.na : p.n0;
             mbar_arrive_expect_tx(bar, (uint32_t)((c1 - c0) * kAtom));
             if (p.whole_rows) {
@@ -329,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       }
       // every requested copy lands before the shared memory is released (bounded; on the normal
       // path nothing is outstanding: the MMA warp has waited for each)
-      if (segs > 0) mbar_wait_bounded(q_full, (uint32_t)((segs - 1) & 1), nullptr);
+      if (segs > 0) mbar_wait_ready(q_full, (uint32_t)((segs - 1) & 1), nullptr);
       for (int piece = 0; piece < pieces; ++piece)
         for (int k = max(0, got[piece] - p.nstage); k < got[piece]; ++k)
-          mbar_wait_bounded(&full[2 * (k % p.nstage) + piece], (uint32_t)((k / p.nstage) & 1), nullptr);
+          mbar_wait_ready(&full[2 * (k % p.nstage) + piece], (uint32_t)((k / p.nstage) & 1), nullptr);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- S issuer
@@ -348,15 +348,15 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       bool ok = true;
       int i = 0, segs = 0, tails = 0;
       while (ok && walk.next(seg)) {
-        ok = mbar_wait_bounded(q_full, (uint32_t)(segs & 1), a.dev_status);
+        ok = mbar_wait_ready(q_full, (uint32_t)(segs & 1), a.dev_status);
         for (int t = seg.t0; ok && t < seg.t1; ++t, ++i, ring.next()) {
           const bool last = (t + 1) * kTok > seg.L;  // not full: what lies past the length is cleared first
-          if (i >= 2 && !(ok = mbar_wait_bounded(&p_full[i & 1], (uint32_t)((i >> 1) & 1) ^ 1u, a.dev_status))) break;
-          if (!(ok = mbar_wait_bounded(&full[2 * ring.st], ring.ph, a.dev_status))) break;
+          if (i >= 2 && !(ok = mbar_wait_ready(&p_full[i & 1], (uint32_t)((i >> 1) & 1) ^ 1u, a.dev_status))) break;
+          if (!(ok = mbar_wait_ready(&full[2 * ring.st], ring.ph, a.dev_status))) break;
           if (last) {
-            if (pieces > 1 && !(ok = mbar_wait_bounded(&full[2 * ring.st + 1], ring.ph, a.dev_status))) break;
+            if (pieces > 1 && !(ok = mbar_wait_ready(&full[2 * ring.st + 1], ring.ph, a.dev_status))) break;
             mbar_arrive(partial);
-            if (!(ok = mbar_wait_bounded(tail, (uint32_t)(tails & 1), a.dev_status))) break;
+            if (!(ok = mbar_wait_ready(tail, (uint32_t)(tails & 1), a.dev_status))) break;
             ++tails;
           }
           tc_fence_after();
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
           };
           blocks(whole0);
           if (pieces > 1) {
-            if (!last && !(ok = mbar_wait_bounded(&full[2 * ring.st + 1], ring.ph, a.dev_status))) break;
+            if (!last && !(ok = mbar_wait_ready(&full[2 * ring.st + 1], ring.ph, a.dev_status))) break;
             tc_fence_after();
             blocks(whole1);
           }
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       // products left by a timeout get a bounded chance to finish; on the normal path this is the
       // end of the last one
       umma_commit(&drain[0]);
-      mbar_wait_bounded(&drain[0], 0u, nullptr);
+      mbar_wait_ready(&drain[0], 0u, nullptr);
     }
   } else if (warp == 3) {
     // ---------------------------------------------------------------- O~ issuer
@@ -407,9 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       bool ok = true;
       int i = 0, segs = 0;
       while (ok && walk.next(seg)) {
-        if (segs > 0) ok = mbar_wait_bounded(o_free, (uint32_t)((segs - 1) & 1), a.dev_status);
+        if (segs > 0) ok = mbar_wait_ready(o_free, (uint32_t)((segs - 1) & 1), a.dev_status);
         for (int t = seg.t0; ok && t < seg.t1; ++t, ++i, ring.next()) {
-          if (!(ok = mbar_wait_bounded(&p_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status))) break;
+          if (!(ok = mbar_wait_ready(&p_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status))) break;
           tc_fence_after();
           uint64_t dt = sw128_mn_desc(stage0 + (uint32_t)ring.st * stage_bytes, kAtom);
           const uint64_t dp = sw128_desc(p_addr);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
         ++segs;
       }
       umma_commit(&drain[1]);
-      mbar_wait_bounded(&drain[1], 0u, nullptr);
+      mbar_wait_ready(&drain[1], 0u, nullptr);
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- rows past the length
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
         };
         bool move = false;
         if (active) {
-          bad |= !mbar_wait_bounded(&s_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status);
+          bad |= !mbar_wait_ready(&s_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status);
           tc_fence_after();
           tmem_ld_16x256b(tmem + lane_addr + kSCol + (uint32_t)(i & 1) * kTok, v);
           tmem_wait_ld();
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
               sm_f[r0 + 8] = f1;
             }
           }
-          bad |= !mbar_wait_bounded(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
+          bad |= !mbar_wait_ready(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
           if (named_bar_or(1, 128, bad)) break;
           tc_fence_after();
           for (int c = 0; c < p.nm * p.NH; c += 16) {
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
         l1 = l1 * f1 + a1;
         if (active) {
           // P's buffer is free once the last tile's product is in
-          if (i >= 1 && !mbar_wait_bounded(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status))
+          if (i >= 1 && !mbar_wait_ready(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status))
             bad = true;
           const uint32_t base = (uint32_t)r0 * 128u + (uint32_t)col * 2u;
 #pragma unroll
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
         sm_m[r0] = m0;
         sm_m[r0 + 8] = m1;
       }
-      if (!bad) bad = !mbar_wait_bounded(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
+      if (!bad) bad = !mbar_wait_ready(&pv_done[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), a.dev_status);
       if (named_bar_or(1, 128, bad)) break;
       tc_fence_after();
       const int n = tiles_of(seg.L);

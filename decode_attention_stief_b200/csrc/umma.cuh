@@ -87,6 +87,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
       : "memory");
 }
 
+// mbar_wait_bounded for barriers that are mostly complete already.
+__device__ __forceinline__ bool mbar_wait_ready(uint64_t* bar, uint32_t parity, uint32_t* dev_status) {
+  return mbar_test(bar, parity) || mbar_wait_bounded(bar, parity, dev_status);
+}
+
 // One arrival on `bar` once every tcgen05 operation this thread issued before has completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
