@@ -591,38 +591,70 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
       float2* ml = reinterpret_cast<float2*>(ws + meta_bytes(a.B)) + (size_t)slot * kMaxHeads;
       float* part = reinterpret_cast<float*>(ws + meta_bytes(a.B) + ml_bytes()) + (size_t)slot * p.NH * a.r;
-      // 32 heads' columns at a time: one wait for two loads, then a run of stores (a warp's 32
-      // neighbouring dims of one head each)
-      for (int m = 0; m < p.nm; ++m) {
-        const int d = m * 128 + dim;
-        for (int c = 0; c < p.NH; c += 32) {
-          uint32_t v[2][16];
-          tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c), v[0]);
-          if (c + 16 < p.NH) tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c + 16), v[1]);
-          tmem_wait_ld();
-          const int nh = d < a.r ? nheads - c : 0;  // heads to store
-          if (whole) {
-            // (all factors first: read between the stores, each load would wait for the last store)
-            float4 f[8];
+      if (whole) {
+        // Half of the heads' 128 dims at a time, through P's memory (free until the next segment): a
+        // thread has one dim of every head, and stored from there, two bytes a lane, the output took
+        // 5 us at 64 heads and r = 512.
+        const int hc = p.NH / 2, th = tid - 128;
+        uint8_t* stage = smem + lay.p;
+        for (int m = 0; m < p.nm; ++m)
+          for (int c = 0; c < p.NH; c += hc) {
+            uint32_t v[2][16];
+            tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c), v[0]);
+            if (hc > 16) tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c + 16), v[1]);
+            float4 f[8];  // 1 / l (the last ones may lie past the heads: they are not used)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = lds128f(smem_u32(sm_f + c + 4 * e));
-            // neighbouring lanes swap halves of each pair of heads: an even lane stores its dim and
-            // the next of the first head, an odd one its dim and the one before of the second
-            const int odd = lane & 1;
-            uint16_t* o = a.out + ((size_t)seg.b * a.Hq + h_base + c + odd) * a.r + d - odd;
+            for (int e = 0; e < 8; ++e)
+              if (4 * e < hc) f[e] = lds128f(smem_u32(sm_f + c + 4 * e));
+            tmem_wait_ld();
+            // (eight heads a branch: hc is a multiple of eight, and a test each made this ten times
+            // as long)
 #pragma unroll
-            for (int e = 0; e < 32; e += 2, o += 2 * (size_t)a.r) {
-              const float4 g = f[e >> 2];
-              const float x0 = __uint_as_float(v[e >> 4][e & 15]) * ((e & 2) ? g.z : g.x);
-              const float x1 = __uint_as_float(v[e >> 4][(e + 1) & 15]) * ((e & 2) ? g.w : g.y);
-              const float y = __shfl_xor_sync(~0u, odd ? x0 : x1, 1);
-              if (e + odd < nh) *reinterpret_cast<uint32_t*>(o) = odd ? pack_bf16x2_rn(y, x1) : pack_bf16x2_rn(x0, y);
-            }
-          } else {
+            for (int e8 = 0; e8 < 32; e8 += 8)
+              if (e8 < hc) {
+#pragma unroll
+                for (int e = e8; e < e8 + 8; ++e) {
+                  const float4 g = f[e >> 2];
+                  const float x = (e & 3) == 0 ? g.x : (e & 3) == 1 ? g.y : (e & 3) == 2 ? g.z : g.w;
+                  *reinterpret_cast<uint16_t*>(stage + e * 256 + dim * 2) =
+                      f32_to_bf16_rn(__uint_as_float(v[e >> 4][e & 15]) * x);
+                }
+              }
+            named_bar_sync(1, 128);
+            const int h0 = th >> 4, d = m * 128 + (th & 15) * 8;  // sixteen lanes a head
+            uint16_t* o = a.out + ((size_t)seg.b * a.Hq + h_base + c + h0) * a.r + d;
+            uint4 y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (8 * k < hc) y[k] = *reinterpret_cast<const uint4*>(stage + (8 * k + h0) * 256 + (th & 15) * 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k, o += 8 * (size_t)a.r)
+              if (8 * k < hc && c + 8 * k + h0 < nheads && d < a.r) *reinterpret_cast<uint4*>(o) = y[k];
+            named_bar_sync(1, 128);
+          }
+      } else {
+        // 32 heads' columns at a time: one wait for two loads, then a run of stores (a warp's 32
+        // neighbouring dims of one head each)
+        for (int m = 0; m < p.nm; ++m) {
+          const int d = m * 128 + dim;
+          for (int c = 0; c < p.NH; c += 32) {
+            uint32_t v[2][16];
+            tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c), v[0]);
+            if (c + 16 < p.NH) tmem_ld16(tmem + lane_addr + (uint32_t)(m * p.NH + c + 16), v[1]);
+            tmem_wait_ld();
+            const int nh = d < a.r ? nheads - c : 0;  // heads to store
             float* o = part + (size_t)c * a.r + d;
 #pragma unroll
-            for (int e = 0; e < 32; ++e, o += a.r)
-              if (e < nh) *o = __uint_as_float(v[e >> 4][e & 15]);
+            for (int e8 = 0; e8 < 32; e8 += 8, o += 8 * (size_t)a.r) {
+              if (e8 + 8 <= nh) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[(size_t)e * a.r] = __uint_as_float(v[(e8 + e) >> 4][(e8 + e) & 15]);
+              } else if (e8 < nh) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (e8 + e < nh) o[(size_t)e * a.r] = __uint_as_float(v[(e8 + e) >> 4][(e8 + e) & 15]);
+              }
+            }
           }
         }
       }
@@ -779,11 +811,10 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   p.stall = test_stall_bytes();
 #endif
   // Short sequences are finished by one CTA each: the second kernel costs 2 us, as much as two
-  // further tiles.  (5 sequences of up to 200 tokens: 7.9 us with it.)
+  // further tiles.  (5 sequences, 16 heads, rank 128: 7.1 us for 256 tokens, 8.7 for 257, split.)
   p.whole = a.max_seq_len <= kWholeTiles * kTok;
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
-  for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage).total > kMost;)
-    --p.nstage;
+  for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage).total > kMost;) --p.nstage;
   uint32_t smem = layout_of(p.na, p.sa, p.NH, p.nstage).total;
   if (smem > kMost) return cudaErrorInvalidValue;
   if (smem < 120u * 1024u) smem = 120u * 1024u;  // one CTA an SM: it holds all of TMEM
@@ -826,8 +857,10 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   if (e != cudaSuccess || p.whole) return e;
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  // many parts a sequence: a CTA's warps share them; else a warp a head
-  if (p.G > 8 * a.B) {
+  // Few sequences, hence many parts each: the warps of a CTA share them, where one wave of such CTAs
+  // holds the whole output; else a warp a head.  (5 sequences of 1024 tokens: 8.7 against 10.5 us
+  // with 16 heads at rank 128; with 64 at rank 512, five waves, 24.9 against 15.2.)
+  if (p.G > 8 * a.B && (long long)a.Hq * p.nm * a.B <= 4LL * a.sms) {
     cfg.blockDim = dim3(512);
     cfg.gridDim = dim3(a.Hq * p.nm, a.B);
     return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<16>, a, p.NH, p.groups, p.G);
