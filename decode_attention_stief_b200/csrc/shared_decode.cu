@@ -27,10 +27,16 @@
 // only for that test, is off the path from S to P.  Weights are rounded to bf16 once, and the sum
 // l adds the rounded weights, so that a weight's rounding cancels where it dominates.
 //
-// Work: the 64-token tiles of all sequences, in order, are dealt out evenly: CTA c takes tiles
-// [c per, (c + 1) per), so ragged batches and single long sequences fill the GPU alike.  A
+// Work: the 64-token tiles of all sequences, in order, are dealt out evenly: CTA c takes what lies
+// in [c per, (c + 1) per), so ragged batches and single long sequences fill the GPU alike.  A
 // sequence inside one CTA is finished there; the others leave (o~, m, l) in fp32 for a second
 // kernel, launched as a programmatic dependent, which also writes the zeros of empty sequences.
+//
+// Measured (rank 512 + 64, outputs and caches larger than L2): one sequence of 32768 tokens, 32
+// heads: 19.5 us, 1.9 TB/s over the call, of it 8 us at 4.7 TB/s for the rows (the rest is the
+// start, the parts and their joining).  64 ragged sequences of up to 4096 tokens: 45 us at 32
+// heads (3.8 TB/s), 76 us at 128, where the two CTAs that share a token's rows hold two tiles
+// each and wait for them: the tensor cores are 40 % busy.
 #include <cstdint>
 
 #include "shared_latent.h"
@@ -446,9 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       if (!__all_sync(~0u, got)) break;
       ++tails;
       uint8_t* tile = smem + lay.stages + (uint32_t)(st * p.sa) * kAtom;
-      for (int c = 0; c < (a.r + 63) / 64; ++c)
-        for (int e = valid * 8 + lane; e < kTok * 8; e += 32)
-          *reinterpret_cast<uint4*>(tile + c * kAtom + e * 16) = make_uint4(0, 0, 0, 0);
+      const int atoms = (a.r + 63) / 64;
+      for (int e = valid * 8 + lane; e < kTok * 8; e += 32)
+#pragma unroll 4
+        for (int c = 0; c < atoms; ++c) *reinterpret_cast<uint4*>(tile + c * kAtom + e * 16) = make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(tail);

@@ -606,9 +606,9 @@ STIEF_API stief_status stief_append_shared_paged(const uint16_t* c_new, const ui
  * over tokens [0, seq_lens[b]).  A sequence of length 0 gives zeros; a length that is negative
  * or above max_seq_len gives zeros and STIEF_DEV_BAD_LENGTH.  Rows at and past the length may
  * hold anything.  Pages that are not mapped read as zeros, as in the paged decode.
- * max_seq_len <= max_pages * page_size, B * ceil(max_seq_len / 64) < 2^30.  workspace: stief_decode_shared_workspace_bytes(B, Hq, r)
- * bytes, 16-byte aligned; its contents do not matter before or after a call, but calls that may
- * overlap must not share it.
+ * max_seq_len <= max_pages * page_size, B * ceil(max_seq_len / 64) < 2^30.  workspace:
+ * stief_decode_shared_workspace_bytes(B, Hq, r) bytes, 16-byte aligned; its contents do not matter
+ * before or after a call, but calls that may overlap must not share it.
  * Products are bf16 on the tensor cores with fp32 sums; the weights enter the second product
  * rounded to bf16 (a relative error of at most 2^-8 each).
  */
@@ -651,9 +651,9 @@ STIEF_API stief_status stief_expand_shared_paged(const uint16_t* pages, const in
  * [0, Nkv), or with more than max_q_len queries, is skipped with STIEF_DEV_BAD_LENGTH.  Output
  * rows of no sequence are left as they were.  d == 128, 0 <= dr <= 64 a multiple of 16,
  * Hq <= 256, B * Hq * ceil(max_q_len / 128) < 2^31.  The weights enter the second product rounded
- * to bf16.  Rows of no sequence, or of
- * another one, may hold anything; a value row of the sequence itself that is not finite may also
- * reach queries of the same sequence that do not see it (as a weight of 0).
+ * to bf16.  Rows of no sequence, or of another one, may hold anything; a value row of the sequence
+ * itself that is not finite may also reach queries of the same sequence that do not see it (as a
+ * weight of 0).
  */
 STIEF_API stief_status stief_prefill_attention(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                               const uint16_t* k_pe, const int32_t* q_start, const int32_t* kv_start,
