@@ -73,6 +73,7 @@ struct Args {
   int nstage;
   int whole_rows;     // w % 64 == 0: one copy brings a tile's atoms
   int whole;          // sequences are not split over CTAs, and there is no second kernel
+  int direct;         // whole, and there is a CTA for each sequence: no sums over the lengths
   float scale2;       // |scale| * log2(e)
   int negate;         // scale < 0: the products are negated instead
 #ifdef STIEF_TEST_HOOKS
@@ -117,12 +118,12 @@ struct Ring {
 
 __device__ __forceinline__ int valid_length(int L, int most) { return L < 0 || L > most ? 0 : L; }
 
-__device__ __forceinline__ int tiles_of(int L) { return (L + kTok - 1) / kTok; }
+__host__ __device__ __forceinline__ int tiles_of(int L) { return (L + kTok - 1) / kTok; }
 
 // Tiles are dealt out by cost: a sequence counts kSegment tiles more than it has, for the query's
 // copy and the output, placed before its first tile.
 constexpr int kSegment = 3;
-constexpr int kWholeTiles = 4;
+constexpr int kWholeTiles = 4, kDirectTiles = 6;  // tiles of sequences that are not split (see the launch)
 
 // The stretch of one sequence's tiles [t0, t1) that a CTA works on.
 struct Segment {
@@ -229,60 +230,76 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
 
   pdl_wait();
   pdl_launch_dependents();
-  // where this CTA's tiles begin: a prefix sum of the sequences' tile counts
-  const int per_thread = (a.B + kThreads - 1) / kThreads, c0 = tid * per_thread, c1 = min(a.B, c0 + per_thread);
-  auto cost_of = [&](int b) {
-    const int n = tiles_of(valid_length(__ldg(a.seq_lens + b), a.max_seq_len));
-    return n > 0 ? n + kSegment : 0;
-  };
-  int sum = 0;
-  for (int b = c0; b < c1; ++b) {
-    const int L = __ldg(a.seq_lens + b);
-    if (valid_length(L, a.max_seq_len) != L && blockIdx.x == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
-    sum += cost_of(b);
-  }
-  int incl = sum;
+  int per = 1, count = 0;  // the CTA's share begins at g0 and costs `count`
+  long long g0 = 0;
+  if (p.direct) {  // a CTA a sequence
+    count = cta < a.B ? 1 : 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (count > 0 && group == 0 && tid == 64) {
+      const int L = __ldg(a.seq_lens + cta);
+      if (valid_length(L, a.max_seq_len) != L) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
+    }
+  } else {
+    // where this CTA's tiles begin: a prefix sum of the sequences' tile counts
+    const int per_thread = (a.B + kThreads - 1) / kThreads, c0 = tid * per_thread, c1 = min(a.B, c0 + per_thread);
+    auto cost_of = [&](int b) {
+      const int n = tiles_of(valid_length(__ldg(a.seq_lens + b), a.max_seq_len));
+      return n > 0 ? n + kSegment : 0;
+    };
+    int sum = 0;
+    for (int b = c0; b < c1; ++b) {
+      const int L = __ldg(a.seq_lens + b);
+      if (valid_length(L, a.max_seq_len) != L && blockIdx.x == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
+      sum += cost_of(b);
+    }
+    int incl = sum;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += u;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  int total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i == warp) incl += total;
-    total += warp_sum[i];
-  }
-  int per = (total + p.G - 1) / p.G;
-  if (per < kMinTiles) per = kMinTiles;
-  const long long g0 = (long long)cta * per;
-  const int count = g0 >= total ? 0 : (int)min((long long)per, total - g0);
-  if (count > 0 && g0 >= incl - sum && g0 < incl) {  // one thread's sequences hold the first tile
-    int at = incl - sum, b = c0;
-    for (;; ++b) {
-      const int n = cost_of(b);
-      if (g0 < at + n) break;
-      at += n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += u;
     }
-    start_b = b;
-    start_off = (int)(g0 - at) - kSegment;  // negative: cost before the first tile
-    if (p.whole && g0 > at) {  // that sequence is another CTA's: begin with the next
-      start_b = b + 1;
-      start_off = -kSegment - (at + cost_of(b) - (int)g0);
+    if (lane == 31) warp_sum[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int total = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i == warp) incl += total;
+      total += warp_sum[i];
     }
+    per = (total + p.G - 1) / p.G;
+    if (per < kMinTiles) per = kMinTiles;
+    g0 = (long long)cta * per;
+    count = g0 >= total ? 0 : (int)min((long long)per, total - g0);
+    if (count > 0 && g0 >= incl - sum && g0 < incl) {  // one thread's sequences hold the first tile
+      int at = incl - sum, b = c0;
+      for (;; ++b) {
+        const int n = cost_of(b);
+        if (g0 < at + n) break;
+        at += n;
+      }
+      start_b = b;
+      start_off = (int)(g0 - at) - kSegment;  // negative: cost before the first tile
+      if (p.whole && g0 > at) {  // that sequence is another CTA's: begin with the next
+        start_b = b + 1;
+        start_off = -kSegment - (at + cost_of(b) - (int)g0);
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
   const uint32_t tmem = tmem_slot;
   Walk walk{a.seq_lens, a.max_seq_len, a.B, 0, 0, 0, count, g0, p.whole != 0};
-  if (count > 0) {
+  if (p.direct) {
+    walk.b = cta;
+    walk.B = min(a.B, cta + 1);
+  } else if (count > 0) {
     walk.b = start_b;
     walk.off = max(0, start_off);
     walk.skip = max(0, -start_off);
   }
-  if (p.whole && count > 0) {  // (what lies before the first sequence of the share is another's)
+  if (p.whole && !p.direct && count > 0) {  // (what lies before the first sequence of the share is another's)
     walk.left -= walk.skip - kSegment;
     walk.at += walk.skip - kSegment;
     walk.skip = kSegment;
@@ -298,15 +315,24 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       int i = 0, segs = 0;
       Ring ring{p.nstage};
       bool ok = true;
+      auto load_q = [&](int b, int segs) {
+        mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128) + (segs == 0 ? stall : 0u));
+        for (int c = 0; c < p.na; ++c)
+          tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, b * a.Hq + h_base, q_full, keep);
+      };
+      int page = 0;
+      if (p.direct) {  // the query and the first page do not wait for the length
+        page = __ldg(a.block_table + (size_t)cta * a.max_pages);
+        load_q(cta, 0);
+      }
       while (ok && walk.next(seg)) {
         if (segs > 0) ok = mbar_wait_ready(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status);
         if (!ok) break;
-        mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128) + (segs == 0 ? stall : 0u));
-        for (int c = 0; c < p.na; ++c)
-          tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, seg.b * a.Hq + h_base, q_full, keep);
+        if (!p.direct) load_q(seg.b, segs);
         ++segs;
         const int32_t* entry = a.block_table + (size_t)seg.b * a.max_pages + seg.t0 * kTok / a.page_size;
-        int in_page = seg.t0 * kTok % a.page_size, page = __ldg(entry);
+        int in_page = seg.t0 * kTok % a.page_size;
+        if (!p.direct) page = __ldg(entry);
         for (int t = seg.t0; t < seg.t1; ++t, ++i, ring.next()) {
           if (in_page == a.page_size) {
             in_page = 0;
@@ -335,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       }
       // every requested copy lands before the shared memory is released (bounded; on the normal
       // path nothing is outstanding: the MMA warp has waited for each)
-      if (segs > 0) mbar_wait_ready(q_full, (uint32_t)((segs - 1) & 1), nullptr);
+      if (segs > 0 || p.direct) mbar_wait_ready(q_full, (uint32_t)(max(segs, 1) - 1) & 1u, nullptr);
       for (int piece = 0; piece < pieces; ++piece)
         for (int k = max(0, got[piece] - p.nstage); k < got[piece]; ++k)
           mbar_wait_ready(&full[2 * (k % p.nstage) + piece], (uint32_t)((k / p.nstage) & 1), nullptr);
@@ -817,9 +843,14 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
 #ifdef STIEF_TEST_HOOKS
   p.stall = test_stall_bytes();
 #endif
-  // Short sequences are finished by one CTA each: the second kernel costs 2 us, as much as two
-  // further tiles.  (5 sequences, 16 heads, rank 128: 7.1 us for 256 tokens, 8.7 for 257, split.)
-  p.whole = a.max_seq_len <= kWholeTiles * kTok;
+  // Short sequences are finished by one CTA each: the parts and the second kernel cost more than a
+  // few further tiles.  With a CTA for each, which then needs no sums over the lengths either, up to
+  // six tiles (5 sequences, 16 heads, rank 128: 6.2 us for four, 0.6 a tile more, split 8.6 to 9.2;
+  // at 64 heads and rank 512 11.2 us for four, 14.4 for five, 16.8 for eight, split 14.4 to 14.7),
+  // otherwise four, as whole sequences are dealt out less evenly.
+  const int most_tiles = tiles_of(a.max_seq_len);
+  p.direct = a.B <= p.G && most_tiles <= kDirectTiles;
+  p.whole = p.direct || most_tiles <= kWholeTiles;
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
   for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage).total > kMost;) --p.nstage;
   uint32_t smem = layout_of(p.na, p.sa, p.NH, p.nstage).total;
