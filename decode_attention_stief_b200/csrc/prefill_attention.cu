@@ -6,6 +6,14 @@
 // What bounds it: the products (2 (256 + dr) operations a visible pair and head) and, nearly as
 // long, one exponential a pair: 16 a cycle on an SM against 4096 multiply-adds.
 //
+// Two kernels.  Without a position part, prefill_one_tile.cu: two CTAs an SM, a tile of 128 query
+// rows each.  With one a CTA's rows are half as long again and two such CTAs have room for one step
+// of 64 keys each: the products with 64 keys read shared memory for longer than they compute, and
+// what is in flight does not cover the way to memory.  So this file's kernel takes two tiles of
+// queries that share steps of 128 keys (launch_prefill below has the rule and both sides of it).
+// 8192 tokens, 32 heads, dr 64: 550 us, 1.25 PFLOP/s, the tensor cores busy for 63 % of it (1.20
+// PFLOP/s under the power cap of a long run).
+//
 // A CTA takes 256 queries of one head as two tiles of 128 and walks the keys in tiles of 128;
 // both products run on tcgen05 with M = N = 128:
 //     S_w = Q_w . K^T      (Q, K in shared memory, K-major, 128-byte swizzle)
@@ -16,9 +24,10 @@
 //   warp 0: TMA producer; warps 1 and 3: MMA issuers of the two tiles; warp 2: zeroes the value
 //   rows past n_k in the last tile (they may hold NaN, and 0 * NaN is NaN); warps 4-7 and 8-11:
 //   softmax of the two tiles, one thread a query row, and the output.
-// The reference of the running maximum moves only when a score passes it by more than 2^8 (as in
-// the decode): a warp then rescales its own rows of O_w, whose last product is complete when S_w
-// of the next tile is, because the products run in order.
+// The reference of the running maximum moves only when a score passes it by more than 2^60
+// (weights and sums are floating-point numbers: a large weight loses nothing): a warp then rescales
+// its own rows of O_w, whose last product is complete when S_w of the next tile is, because the
+// products run in order.
 // CTAs start with the longest tiles of queries; a tile of queries none of whose rows exists ends
 // at once.
 #include <cstdint>
@@ -33,21 +42,21 @@ namespace {
 
 constexpr int kRows = 128;                 // queries a tile, keys a tile
 constexpr uint32_t kAtom = kRows * 128;    // bytes of 128 rows x 64 columns
-constexpr float kRescale = 8.f;
+constexpr float kRescale = 60.f;           // log2 units a score may pass the reference by
 constexpr float kFloor = -1e30f;
-constexpr int kMaxHalves = 4;  // (no more: a tile's barrier, one of two in turn, is armed again only
-                               // after a wait for the halves of two tiles before)
+constexpr int kAtoms = 3;                  // of 64 columns in a query row
+// Slots of 64 value rows: what fits.  (Not above 4: a tile's barrier, one of two in turn, is armed again
+// only after a wait for the halves of two tiles before.)
+constexpr int kHalves = 3;
 constexpr uint32_t kKeys = 2 * kAtom;      // bytes of a key tile without the position part
 constexpr uint32_t kHalf = kAtom;          // bytes of 64 value rows (two atoms of 64 columns)
 
 struct Args {
-  CUtensorMap mq;   // q [Nq][Hq * (128 + dr)], box 64 x 128
+  CUtensorMap mq;   // q [Nq][Hq * (128 + dr)], box 64 x 128 (dr > 0)
   CUtensorMap mk;   // k [Nkv] rows in blocks of 64 columns, box 64 x 128 x 2
   CUtensorMap mv;   // v, box 64 x 64 x 2
   CUtensorMap mp;   // k_pe [Nkv][dr], box 64 x 128
   PrefillArgs a;
-  int atoms;        // 64-column atoms of a query row: 2, or 3 with a position part
-  int nv;           // slots of 64 value rows
   int qtiles;       // tiles of 256 queries of the longest sequence
   float scale2;     // |scale| * log2(e)
   int negate;       // scale < 0: the products are negated instead
@@ -56,53 +65,33 @@ struct Args {
 #endif
 };
 
-// Queries (kW tiles), key slots, one slot of position parts, slots of 64 value rows.  A key tile's
+// Two tiles of queries, two slots of keys, one of position parts, slots of 64 value rows.  A key tile's
 // position part is wanted between its two products only, so one slot of it is enough, and what
 // that saves holds a third half tile of values: with two, the next one arrived too late.
-struct Layout {
-  uint32_t k, pe, v, bars, total;
-};
-template <int kW>
-__host__ __device__ inline Layout layout_of(int atoms, int nv) {
-  Layout l;
-  l.k = (uint32_t)(kW * atoms) * kAtom;
-  l.pe = l.k + kW * kKeys;  // (as many key slots as tiles of queries)
-  l.v = l.pe + (uint32_t)(atoms - 2) * kAtom;
-  l.bars = l.v + (uint32_t)nv * kHalf;
-  l.total = l.bars + 8 * (4 + 2 + kMaxHalves + 16);
-  return l;
-}
+constexpr uint32_t kSmemK = 2 * kAtoms * kAtom, kSmemPe = kSmemK + 2 * kKeys, kSmemV = kSmemPe + kAtom;
+constexpr uint32_t kSmemBars = kSmemV + kHalves * kHalf, kSmem = kSmemBars + 8 * (6 + kHalves + 12);
+static_assert(kSmem <= kMaxSmemPerBlock - 1024, "one CTA's shared memory, beside the static part");
 
 }  // namespace
 
-template <int kW>
-__global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
-    stief_prefill_kernel(const __grid_constant__ Args p) {
-  constexpr uint32_t kTmemCols = kW * 256;   // S_w at 128 w, O_w at 128 (kW + w)
-  constexpr uint32_t kOCol = kW * 128;
-  constexpr int kKeySlots = kW;
-  // With one tile of queries the product with the first 64 keys starts when half of P is there (its
-  // memory is free, and the next values under way, that much sooner).  Two tiles that share the
-  // keys fall into step that way, and the tensor cores wait for both softmaxes at once: 8192
-  // tokens took 625 us with halves, 550 without.
-  constexpr bool kHalves = kW == 1;
+__global__ void __launch_bounds__(384, 1) stief_prefill_kernel(const __grid_constant__ Args p) {
+  constexpr uint32_t kTmemCols = 512;  // S_w at 128 w, O_w at 256 + 128 w
+  constexpr uint32_t kOCol = 256;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t tmem_slot;
   const PrefillArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Layout lay = layout_of<kW>(p.atoms, p.nv);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + lay.bars);
-  uint64_t* k_empty = k_full + kKeySlots;
-  uint64_t* v_full = k_empty + kKeySlots;   // [2] both halves of a value tile, tiles in turn
-  uint64_t* v_empty = v_full + 2;           // [halves]
-  uint64_t* q_full = v_empty + kMaxHalves;  // [2]
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + kSmemBars);  // [2]
+  uint64_t* k_empty = k_full + 2;           // [2]
+  uint64_t* v_full = k_full + 4;            // [2] both halves of a value tile, tiles in turn
+  uint64_t* v_empty = k_full + 6;           // [kHalves]
+  uint64_t* q_full = v_empty + kHalves;     // [2]
   uint64_t* s_full = q_full + 2;            // [2] S_w of a tile is in TMEM (and O_w before it)
-  uint64_t* p_half = q_full + 4;            // [2] P_w of the tile's first 64 keys is in TMEM
-  uint64_t* p_full = q_full + 6;            // [2] all of it
-  uint64_t* o_full = q_full + 8;            // [2] O_w is complete
-  uint64_t* partial = q_full + 10;          // the last value tile is in and is not full
-  uint64_t* tail = q_full + 11;             // its rows past n_k are cleared
-  uint64_t* drain = q_full + 12;            // [2]
+  uint64_t* p_full = q_full + 4;            // [2] P_w of a tile is
+  uint64_t* o_full = q_full + 6;            // [2] O_w is complete
+  uint64_t* partial = q_full + 8;           // the last value tile is in and is not full
+  uint64_t* tail = q_full + 9;              // its rows past n_k are cleared
+  uint64_t* drain = q_full + 10;            // [2]
 
 #ifdef STIEF_TEST_HOOKS
   const uint32_t stall = p.stall;
@@ -125,12 +114,12 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
     if (tid == 0 && h == 0 && qt == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
     return;
   }
-  const int nq = q1 - q0, n_k = k1 - k0, first = qt * kW * kRows;
+  const int nq = q1 - q0, n_k = k1 - k0, first = qt * 2 * kRows;
   if (first >= nq) return;
   // key tiles that each tile of queries sees: up to its last row's last key
   int nt[2] = {0, 0};
 #pragma unroll
-  for (int w = 0; w < kW; ++w) {
+  for (int w = 0; w < 2; ++w) {
     const int begin = first + w * kRows, last = min(nq, begin + kRows) - 1;  // last row
     const long long seen = begin < nq ? (long long)last + n_k - nq + 1 : 0;
     nt[w] = seen > 0 ? (int)((min(seen, (long long)n_k) + kRows - 1) / kRows) : 0;
@@ -141,21 +130,20 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
     // a slot is empty when both tiles of queries have read it.  (Where one of them sees a key tile
     // less, that is the last one, whose slot nobody waits for.)
     const uint32_t users = (nt[0] > 0) + (nt[1] > 0);
-    for (int i = 0; i < kKeySlots; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], users);
     }
-    for (int i = 0; i < kMaxHalves; ++i) mbar_init(&v_empty[i], users);
+    for (int i = 0; i < kHalves; ++i) mbar_init(&v_empty[i], users);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&v_full[w], 1);
       mbar_init(&q_full[w], 1);
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_half[w], 4);
       mbar_init(&p_full[w], 4);
       mbar_init(&o_full[w], 1);
       mbar_init(&drain[w], 1);
     }
-    mbar_init(partial, (nt[0] == tiles) + (kW == 2 && nt[1] == tiles));
+    mbar_init(partial, (nt[0] == tiles) + (nt[1] == tiles));
     mbar_init(tail, 1);
     fence_barrier_init();
   }
@@ -169,58 +157,56 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
   const uint32_t tmem = tmem_slot;
 
   if (warp < 4) {
-    // (the shares add up to what the block was launched with: 3 x 168, or 2 x 128)
-    if (kW == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // (the shares add up to what the block was launched with: 3 x 168)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // -------------------------------------------------------------- producer
       if (elect_one()) {
         const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
         const int dq = 128 + a.dr;
         int nkl = 0, nvl = 0;  // key tiles and value halves requested
-        const bool half[2] = {nt[0] > 0, nt[1] > 0}, pos = p.atoms > 2;
+        const bool half[2] = {nt[0] > 0, nt[1] > 0};
         auto load_q = [&](int w) {
-          mbar_arrive_expect_tx(&q_full[w], (uint32_t)p.atoms * kAtom + stall);
-          for (int c = 0; c < p.atoms; ++c)
-            tma_load_2d(smem + (uint32_t)(w * p.atoms + c) * kAtom, &p.mq, h * dq + 64 * c, q0 + first + w * kRows,
+          mbar_arrive_expect_tx(&q_full[w], (uint32_t)kAtoms * kAtom + stall);
+          for (int c = 0; c < kAtoms; ++c)
+            tma_load_2d(smem + (uint32_t)(w * kAtoms + c) * kAtom, &p.mq, h * dq + 64 * c, q0 + first + w * kRows,
                         &q_full[w], once);
         };
         int vs = 0;
         uint32_t vp = 0;  // parity of the half's current use
         bool ok = true;
         for (int i = 0; ok && i < tiles; ++i) {
-          const int row = k0 + i * kRows, ks = i % kKeySlots;
+          const int row = k0 + i * kRows, ks = i % 2;
           if (i == 0 && half[0]) load_q(0);
-          if (i >= kKeySlots && !(ok = mbar_wait_ready(&k_empty[ks], (uint32_t)(i / kKeySlots & 1) ^ 1u, a.dev_status))) break;
-          mbar_arrive_expect_tx(&k_full[ks], kKeys + (pos ? kAtom : 0u));
-          tma_load_3d(smem + lay.k + (uint32_t)ks * kKeys, &p.mk, 0, row, hk * 2, &k_full[ks], keep);
+          if (i >= 2 && !(ok = mbar_wait_ready(&k_empty[ks], (uint32_t)(i / 2 & 1) ^ 1u, a.dev_status))) break;
+          mbar_arrive_expect_tx(&k_full[ks], kKeys + kAtom);
+          tma_load_3d(smem + kSmemK + (uint32_t)ks * kKeys, &p.mk, 0, row, hk * 2, &k_full[ks], keep);
           ++nkl;
-          if (pos) {  // (its one slot is free when the last tile's keys are)
-            if (i > 0) ok = mbar_wait_ready(&k_empty[(i - 1) % kKeySlots], (uint32_t)((i - 1) / kKeySlots & 1), a.dev_status);
-            tma_load_2d(smem + lay.pe, &p.mp, 0, row, &k_full[ks], keep);  // (after a timeout too: it is expected)
-            if (!ok) break;
-          }
+          // (the one slot of position parts is free when the last tile's keys are)
+          if (i > 0) ok = mbar_wait_ready(&k_empty[(i - 1) % 2], (uint32_t)((i - 1) / 2 & 1), a.dev_status);
+          tma_load_2d(smem + kSmemPe, &p.mp, 0, row, &k_full[ks], keep);  // (after a timeout too: it is expected)
+          if (!ok) break;
           if (i == 0 && half[1]) load_q(1);
           for (int c = 0; c < 2; ++c) {
-            if (nvl >= p.nv && ok) ok = mbar_wait_ready(&v_empty[vs], vp ^ 1u, a.dev_status);
+            if (nvl >= kHalves && ok) ok = mbar_wait_ready(&v_empty[vs], vp ^ 1u, a.dev_status);
             if (!ok && c == 0) break;
             if (c == 0) mbar_arrive_expect_tx(&v_full[i & 1], 2 * kHalf);
-            tma_load_3d(smem + lay.v + (uint32_t)vs * kHalf, &p.mv, 0, row + 64 * c, hk * 2, &v_full[i & 1], keep);
+            tma_load_3d(smem + kSmemV + (uint32_t)vs * kHalf, &p.mv, 0, row + 64 * c, hk * 2, &v_full[i & 1], keep);
             ++nvl;
-            if (++vs == p.nv) vs = 0, vp ^= 1u;
+            if (++vs == kHalves) vs = 0, vp ^= 1u;
           }
         }
         // every requested copy lands before the shared memory is released
         if (tiles > 0) {
           for (int w = 0; w < 2; ++w)
             if (half[w]) mbar_wait_ready(&q_full[w], 0, nullptr);
-          for (int j = max(0, nkl - kKeySlots); j < nkl; ++j)
-            mbar_wait_ready(&k_full[j % kKeySlots], (uint32_t)(j / kKeySlots & 1), nullptr);
+          for (int j = max(0, nkl - 2); j < nkl; ++j)
+            mbar_wait_ready(&k_full[j % 2], (uint32_t)(j / 2 & 1), nullptr);
           for (int j = max(0, nvl / 2 - 2); j < nvl / 2; ++j)
             mbar_wait_ready(&v_full[j & 1], (uint32_t)((j >> 1) & 1), nullptr);
         }
       }
-    } else if (warp == 1 || (kW == 2 && warp == 3)) {
+    } else if (warp == 1 || warp == 3) {
       // -------------------------------------------------------------- MMA issuers, one a query tile
       // (one thread for both spent a third of its time testing barriers, which costs hundreds of
       // cycles while the products read shared memory, and kept the other tile's products waiting)
@@ -228,18 +214,18 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
       if (n > 0 && elect_one()) {
         const uint32_t id_s = idesc_bf16_f32(128, 128, false, false) | (p.negate ? 1u << 13 : 0u);
         const uint32_t id_o = idesc_bf16_f32(128, 128, false, true);
-        const uint32_t k_addr = smem_u32(smem + lay.k), v_addr = smem_u32(smem + lay.v);
+        const uint32_t k_addr = smem_u32(smem + kSmemK), v_addr = smem_u32(smem + kSmemV);
         const uint32_t s_col = tmem + (uint32_t)w * 128u, o_col = s_col + kOCol;
-        const uint64_t dq = sw128_desc(smem_u32(smem) + (uint32_t)(w * p.atoms) * kAtom);
-        const uint64_t dp = sw128_desc(smem_u32(smem + lay.pe));
+        const uint64_t dq = sw128_desc(smem_u32(smem) + (uint32_t)(w * kAtoms) * kAtom);
+        const uint64_t dp = sw128_desc(smem_u32(smem + kSmemPe));
         const int pe_steps = a.dr / 16;
         int va = 0;
         auto wait_k = [&](int i) -> bool {
-          return mbar_wait_ready(&k_full[i % kKeySlots], (uint32_t)(i / kKeySlots & 1), a.dev_status);
+          return mbar_wait_ready(&k_full[i % 2], (uint32_t)(i / 2 & 1), a.dev_status);
         };
         auto issue_s = [&](int i) {
           tc_fence_after();
-          const uint64_t dk = sw128_desc(k_addr + (uint32_t)(i % kKeySlots) * kKeys);
+          const uint64_t dk = sw128_desc(k_addr + (uint32_t)(i % 2) * kKeys);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma_bf16(s_col, dq + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2, dk + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2,
@@ -247,43 +233,36 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
           for (int kk = 0; kk < pe_steps; ++kk)
             umma_bf16(s_col, dq + 2 * (kAtom >> 4) + 2 * kk, dp + 2 * kk, id_s, 1);
           umma_commit(&s_full[w]);
-          umma_commit(&k_empty[i % kKeySlots]);
+          umma_commit(&k_empty[i % 2]);
         };
         bool ok = mbar_wait_ready(&q_full[w], 0, a.dev_status) && wait_k(0);
         // (the second tile starts when the first has its weights: half a turn behind it)
-        if (kW == 2 && w == 1 && nt[0] > 0 && ok) ok = mbar_wait_ready(&p_full[0], 0, a.dev_status);
+        if (w == 1 && nt[0] > 0 && ok) ok = mbar_wait_ready(&p_full[0], 0, a.dev_status);
         if (ok) issue_s(0);
         for (int i = 0; ok && i < n; ++i) {
-          const int vb = va + 1 == p.nv ? 0 : va + 1;
+          const int vb = va + 1 == kHalves ? 0 : va + 1;
           if (!(ok = mbar_wait_ready(&v_full[i & 1], (uint32_t)((i >> 1) & 1), a.dev_status))) break;
           if (i == tiles - 1 && (i + 1) * kRows > n_k) {  // rows past n_k must not be NaN
             mbar_arrive(partial);
             if (!(ok = mbar_wait_ready(tail, 0, a.dev_status))) break;
           }
-          // With a CTA to itself a tile of queries waits for its next keys while the softmax runs: a
-          // test of a barrier takes some 250 cycles next to the products' shared-memory traffic.
-          // Two tiles that share keys do it later: the next position part comes only when both have
-          // their products with this one.
-          if (kW == 1 && i + 1 < n && !(ok = wait_k(i + 1))) break;
           const uint64_t dva = sw128_mn_desc(v_addr + (uint32_t)va * kHalf, kHalf / 2);
           const uint64_t dvb = sw128_mn_desc(v_addr + (uint32_t)vb * kHalf, kHalf / 2);
-          if (!(ok = mbar_wait_ready(kHalves ? &p_half[w] : &p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
+          if (!(ok = mbar_wait_ready(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(o_col, s_col + kk * 8, dva + kk * 128, id_o, i > 0 || kk > 0);
           umma_commit(&v_empty[va]);
-          if (kHalves && !(ok = mbar_wait_ready(&p_full[w], (uint32_t)(i & 1), a.dev_status))) break;
-          tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(o_col, s_col + 32 + kk * 8, dvb + kk * 128, id_o, 1);
           umma_commit(&v_empty[vb]);
           if (i + 1 < n) {
-            if (kW == 2 && !(ok = wait_k(i + 1))) break;
+            if (!(ok = wait_k(i + 1))) break;
             issue_s(i + 1);
           } else {
             umma_commit(&o_full[w]);
           }
-          va = vb + 1 == p.nv ? 0 : vb + 1;
+          va = vb + 1 == kHalves ? 0 : vb + 1;
         }
         // products left by a timeout get a bounded chance to finish; on the normal path this is
         // the end of the last one
@@ -299,7 +278,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
         if (__all_sync(~0u, got)) {
           const int valid = n_k - (tiles - 1) * kRows;
           for (int half = 0; half < 2; ++half) {
-            uint8_t* v = smem + lay.v + (uint32_t)((2 * tiles - 2 + half) % p.nv) * kHalf;
+            uint8_t* v = smem + kSmemV + (uint32_t)((2 * tiles - 2 + half) % kHalves) * kHalf;
             for (int c = 0; c < 2; ++c)
               for (int e = max(0, valid - 64 * half) * 8 + lane; e < 64 * 8; e += 32)
                 *reinterpret_cast<uint4*>(v + c * (kHalf / 2) + e * 16) = make_uint4(0, 0, 0, 0);
@@ -312,8 +291,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
     }
   } else {
     // ---------------------------------------------------------------- softmax and output
-    if (kW == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int w = (warp - 4) >> 2, quad = warp & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t s_col = tmem + lanes + (uint32_t)w * 128u, o_col = tmem + lanes + kOCol + (uint32_t)w * 128u;
@@ -385,12 +363,6 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
           w16[e] = pack_bf16x2_rn(lo, hi);
         }
         tmem_st16(s_col + 16 * c, w16);
-        if (kHalves && c == 1) {
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_half[w]);
-        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -406,7 +378,7 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
       // The rows go through the warp's part of the queries' memory (their last product is done), so
       // that half a warp stores a whole row: stored by the thread that holds it, in pieces of 16
       // bytes, a row took five times as long.  A row's 16-byte pieces are rotated by its number.
-      uint8_t* stage = smem + (uint32_t)(w * p.atoms) * kAtom + (uint32_t)quad * 32 * 256;
+      uint8_t* stage = smem + (uint32_t)(w * kAtoms) * kAtom + (uint32_t)quad * 32 * 256;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t v[32];
@@ -446,14 +418,10 @@ __global__ void __launch_bounds__(kW == 2 ? 384 : 256, kW == 2 ? 1 : 2)
 
 namespace {
 
-template <int kW>
-cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
+cudaError_t launch_two_tiles(const PrefillArgs& a, cudaStream_t stream) {
   Args p{};
   p.a = a;
-  p.atoms = a.dr > 0 ? 3 : 2;
-  constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
-  for (p.nv = kW == 1 ? 2 : kMaxHalves; layout_of<kW>(p.atoms, p.nv).total > kMost;) --p.nv;
-  p.qtiles = (a.max_q + kW * kRows - 1) / (kW * kRows);
+  p.qtiles = (a.max_q + 2 * kRows - 1) / (2 * kRows);
   p.scale2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
   if (p.scale2 < 1e-30f) p.scale2 = 1e-30f;  // above 0, so that a masked score stays -inf
   p.negate = a.scale < 0;
@@ -462,40 +430,45 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t stream) {
 #endif
   const long long blocks = (long long)p.qtiles * a.Hq * a.B;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const uint32_t smem = layout_of<kW>(p.atoms, p.nv).total;
   const uint64_t rows = a.Nkv > 0 ? a.Nkv : 1;  // (no keys: the maps are never used)
   const void* k = a.Nkv > 0 ? a.k : a.q;
   const void* v = a.Nkv > 0 ? a.v : a.q;
-  const void* pe = a.Nkv > 0 && a.dr > 0 ? a.pe : a.q;
-  const uint64_t dq = (uint64_t)a.Hq * (128 + a.dr), dk = (uint64_t)a.Hkv * 128, dp = a.dr > 0 ? a.dr : 64;
+  const void* pe = a.Nkv > 0 ? a.pe : a.q;
+  const uint64_t dq = (uint64_t)a.Hq * (128 + a.dr), dk = (uint64_t)a.Hkv * 128, dp = a.dr;
   if (!encode_tiled_bf16_2d(&p.mq, a.q, dq, (uint64_t)a.Nq, dq * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tiled_bf16_3d(&p.mk, k, {64, rows, dk / 64}, {dk * 2, 128}, {64, kRows, 2}) ||
       !encode_tiled_bf16_3d(&p.mv, v, {64, rows, dk / 64}, {dk * 2, 128}, {64, kRows / 2, 2}) ||
-      !encode_tiled_bf16_2d(&p.mp, pe, dp, a.dr > 0 ? rows : 1, dp * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
+      !encode_tiled_bf16_2d(&p.mp, pe, dp, rows, dp * 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const auto kern = stief_prefill_kernel<kW>;
   static SmemLimit limit;
-  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kern), a.device, (int)smem);
+  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_prefill_kernel), a.device, (int)kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kW == 2 ? 384 : 256);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(384);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return cudaLaunchKernelEx(&cfg, stief_prefill_kernel, p);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
-  // Without a position part a CTA of one tile of queries takes 97 KB, and two of them share an SM:
-  // one's start and end overlap the other's products.  With it only one CTA fits, of two tiles.
-  return a.dr > 0 ? launch<2>(a, stream) : launch<1>(a, stream);
+  // Query heads that share a KV head go into the rows of one tile (8 prompts of 65 to 1500 queries,
+  // 32 heads over 8: 84.9 us against 109.5 with a head a tile and steps of 128 keys).
+  const int group = a.Hq / a.Hkv, pack = group <= kRows && (group & (group - 1)) == 0 ? group : 1;
+  // With a position part one tile of queries a CTA is for prompts that do not fill more than one:
+  // 8 chunks of 128 over 4128 keys, 32 heads, 116 us against 150; but 8 of 256, 229 against 182.  And
+  // then only if there are more CTAs than SMs or few keys: 1 chunk of 128 over 8128 keys, 128 heads,
+  // 182 us against 132; 5 prompts of up to 64, 6.0 against 7.9.
+  const bool small = (long long)a.max_q * pack <= kRows &&
+                     ((long long)a.B * (a.Hq / pack) > a.sms || a.Nkv <= 512LL * a.B);
+  return a.dr == 0 || small ? launch_prefill_one_tile(a, pack, stream) : launch_two_tiles(a, stream);
 }
 
 }  // namespace stief

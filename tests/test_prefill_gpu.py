@@ -87,6 +87,42 @@ def test_prefill_peaked_and_flat_scores(scale):
     _check(got, q, k, v, pe, [0, 400], [0, 400], scale)
 
 
+@pytest.mark.parametrize("scale", [1.0, -0.5])
+@pytest.mark.parametrize("nq,dr", [(400, 0), (30, 16), (400, 16)])
+def test_prefill_late_peaks(nq, dr, scale):
+    """The largest scores come last and far above the first ones: the running reference moves."""
+    q, k, v, pe = _inputs([nq], [400], 8, 2, dr, 78)
+    k *= torch.linspace(0.2, 4.0, 400, device=DEV)[:, None, None].to(torch.bfloat16)
+    k[:, :, 0] = torch.linspace(0.0, 9.0, 400, device=DEV)[:, None].to(torch.bfloat16) * (1 if scale > 0 else -1)
+    q[:, :, 0] = 20.0
+    got = _prefill(q, k, v, pe, [0, nq], [0, 400], nq, scale)
+    _check(got, q, k, v, pe, [0, nq], [0, 400], scale)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(16, 1), (12, 4), (128, 1), (256, 1), (64, 2), (130, 65)])
+@pytest.mark.parametrize("dr", [0, 16])
+def test_prefill_shared_heads(Hq, Hkv, dr):
+    """Groups of query heads that fill a tile's rows, part of them, or do not divide them; sequences
+    that end inside a tile, with fewer queries than a tile has room for and with more."""
+    for nq, nk in (([9, 1, 0, 33], [9, 90, 5, 20]), ([1] * 4, [1, 64, 65, 300]), ([130], [131])):
+        q, k, v, pe = _inputs(nq, nk, Hq, Hkv, dr, Hq + dr, pad=2)
+        qs, ks = _starts(nq, 1), _starts(nk, 1)
+        got = _prefill(q, k, v, pe, qs, ks, max(nq), 0.1)
+        _check(got, q, k, v, pe, qs, ks, 0.1)
+        assert torch.all(got[: qs[0]] == 7.0) and torch.all(got[qs[-1]:] == 7.0)
+
+
+@pytest.mark.parametrize("B,nk", [(6, 700), (2, 700), (3, 100)])
+def test_prefill_short_chunks_with_positions(B, nk):
+    """Chunks within one tile of queries: many, few, and few over few keys."""
+    nq = [128, 1, 65, 17, 0, 100][:B]
+    keys = [nk + b for b in range(B)]
+    q, k, v, pe = _inputs(nq, keys, 32, 32, 64, B + nk)
+    qs, ks = _starts(nq), _starts(keys)
+    got = _prefill(q, k, v, pe, qs, ks, 128, 0.09)
+    _check(got, q, k, v, pe, qs, ks, 0.09)
+
+
 def test_prefill_masked_places_hold_nan_and_infinities():
     """Keys and values that no query of a sequence sees belong to its neighbours in the arrays:
     what stands there must not matter."""
