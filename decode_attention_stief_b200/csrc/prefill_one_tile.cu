@@ -22,8 +22,13 @@
 // it by more than 2^60 (weights and sums are floating-point numbers: a large weight loses nothing);
 // the warp then rescales its rows of O, once the last product is done.
 //
-// What bounds it, a step and CTA: the exponentials (16 a cycle on an SM: 512 cycles) and the products
-// (640: with 64 keys the first one reads shared memory for 48 cycles where it computes for 32).
+// What bounds it: shared memory.  A step's products read 64 KB of it (the queries for every 64 keys
+// anew) and its copies write 32: 768 cycles at 128 bytes a cycle, where the products alone would take
+// 512 and the exponentials, 16 a cycle on an SM, another 512 beside them.  Of the some 1900 cycles that
+// a step of both CTAs takes that is 80 %; the tensor cores are busy for 47 % (chunks) of the time.
+// (Two tiles of queries that share the keys read and write a third less, but their CTA has an SM to
+// itself and no second buffer of scores: 8 chunks of 512 over 3012 keys 208 us against 238, but 2500
+// tokens 69 against 57.5, and 8 chunks of 128 over 4128 keys 134 against 89.)
 // Measured: 8192 tokens, 32 heads over 8: 456 us, 1.21 PFLOP/s; 8 prompts of 65 to 1500: 84.9 us,
 // 0.74 PFLOP/s (its diagonal tiles compute twice what is counted); 5 prompts of up to 64: 5.7 us.
 #include <cstdint>
