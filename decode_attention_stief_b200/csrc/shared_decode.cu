@@ -35,8 +35,10 @@
 // Measured (rank 512 + 64, outputs and caches larger than L2): one sequence of 32768 tokens, 32
 // heads: 19.5 us, 1.9 TB/s over the call, of it 8 us at 4.7 TB/s for the rows (the rest is the
 // start, the parts and their joining).  64 ragged sequences of up to 4096 tokens: 45 us at 32
-// heads (3.8 TB/s), 76 us at 128, where the two CTAs that share a token's rows hold two tiles
-// each and wait for them: the tensor cores are 40 % busy.
+// heads (3.8 TB/s), 49 at 64, 76 at 128.  There shared memory is what most is asked of: a tile's
+// copies write 72 KB of it and its products read 240, 2500 cycles at 128 bytes a cycle, of the some
+// 4000 that a tile takes with two in turn (64 heads' queries leave room for no third; the tensor
+// cores are 40 % busy).  The way to memory is not: tiles brought into L2 two ahead, 77 us.
 #include <cstdint>
 
 #include "shared_latent.h"
