@@ -421,7 +421,7 @@ namespace {
 cudaError_t launch_two_tiles(const PrefillArgs& a, cudaStream_t stream) {
   Args p{};
   p.a = a;
-  p.qtiles = (a.max_q + 2 * kRows - 1) / (2 * kRows);
+  p.qtiles = (int)((a.max_q + 2LL * kRows - 1) / (2 * kRows));
   p.scale2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
   if (p.scale2 < 1e-30f) p.scale2 = 1e-30f;  // above 0, so that a masked score stays -inf
   p.negate = a.scale < 0;

@@ -399,7 +399,7 @@ cudaError_t launch(const PrefillArgs& a, int pack, cudaStream_t stream) {
   p.pack = pack;
   while ((1 << p.shift) < p.pack) ++p.shift;
   const int queries = kRows / p.pack;
-  p.qtiles = (a.max_q + queries - 1) / queries;
+  p.qtiles = (int)((a.max_q + (long long)queries - 1) / queries);
   p.scale2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
   if (p.scale2 < 1e-30f) p.scale2 = 1e-30f;  // above 0, so that a masked score stays -inf
   p.negate = a.scale < 0;

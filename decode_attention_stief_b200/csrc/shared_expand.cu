@@ -13,14 +13,16 @@
 // order, heads innermost: a CTA keeps its rows in shared memory (two row tiles where they fit) and
 // streams the weights' 64-column chunks through a ring.
 //   warp 0: TMA producer; warp 1 of the first CTA: MMA issuer; warps 4-7 store the keys, warps 8-11
-//   the values, through 4 KB of shared memory each, so that eight lanes store 128 neighbouring
-//   bytes of a token (stored by the thread that holds it, 32 bytes at a time, the weights' copies
-//   waited behind the stores).  The unit of head 0 also copies the position values.
+//   the values, through 4 KB (or 2) of shared memory each by TMA, or, where the sequence ends inside,
+//   by eight lanes a token (stored by the thread that holds it, 32 bytes at a time, the weights'
+//   copies waited behind the stores; all of it by eight lanes a token, r 128 took 17.8 us, by TMA
+//   17.2, r 256 24.5 and 23.5).  The unit of head 0 also copies the position values.
 // Row tiles begin at multiples of 128 tokens of their sequence, hence at multiples of 64 rows of
 // a page: two copies bring 64 rows each.
 //
 // Measured: 4096 tokens x 32 heads, r 512: 36.8 us, 0.93 PFLOP/s (29 to 33 us where the 67 MB of output
-// stay in L2), the tensor cores busy for 49 %; 3 sequences of 33 to 501 tokens, 8 heads, r 96: 7.4 us.
+// stay in L2), the tensor cores busy for 49 %; 128 heads:
+// 116 us, 1.19 PFLOP/s; 3 sequences of 33 to 501 tokens, 8 heads, r 96: 7.4 us.
 #include <cstdint>
 
 #include "shared_latent.h"
@@ -34,7 +36,6 @@ namespace {
 constexpr int kRows = 128;                  // tokens a row tile
 constexpr uint32_t kAtomA = kRows * 128;    // 128 rows x 64 columns
 constexpr uint32_t kStageB = 128 * 128;     // 128 weight rows x 64 columns
-constexpr uint32_t kOutWarp = 32 * 128;     // an output warp's 32 tokens x 64 values
 constexpr int kThreads = 384;
 constexpr int kMaxStages = 6;
 constexpr uint32_t kTmemCols = 512;
@@ -42,8 +43,10 @@ constexpr uint32_t kTmemCols = 512;
 struct Args {
   CUtensorMap mc;        // pool [rows][w], box 64 x 64
   CUtensorMap mwk, mwv;  // W [H * 128][r], box 64 x 128
+  CUtensorMap mk, mv;    // outputs [N][H][128], box 64 columns x 1 x out_rows tokens
   SharedExpandArgs a;
   int chunks, na, nb;    // 64-column chunks of r, row tiles and weight chunks held
+  int out_rows;          // tokens that an output warp stages at a time: 32 or 16
 #ifdef STIEF_TEST_HOOKS
   uint32_t stall;     // test build: bytes expected of the first copy that none delivers
 #endif
@@ -52,11 +55,11 @@ struct Args {
 struct Layout {
   uint32_t b, out, bars, total;
 };
-__host__ __device__ inline Layout layout_of(int chunks, int na, int nb) {
+__host__ __device__ inline Layout layout_of(int chunks, int na, int nb, int out_rows) {
   Layout l;
   l.b = (uint32_t)(na * chunks) * kAtomA;
   l.out = l.b + (uint32_t)nb * kStageB;
-  l.bars = l.out + 8 * kOutWarp;
+  l.bars = l.out + (uint32_t)(8 * out_rows) * 128;
   l.total = l.bars + 8 * (2 * kMaxStages + 12);
   return l;
 }
@@ -132,7 +135,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
   __shared__ int warp_sum[kThreads / 32], start_b, start_j;
   const SharedExpandArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Layout lay = layout_of(p.chunks, p.na, p.nb);
+  const Layout lay = layout_of(p.chunks, p.na, p.nb, p.out_rows);
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   // (the full barriers and d_empty that count are the leader's; the others are each CTA's own)
@@ -169,6 +172,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
     prefetch_tensormap(&p.mc);
     prefetch_tensormap(&p.mwk);
     prefetch_tensormap(&p.mwv);
+    prefetch_tensormap(&p.mk);
+    prefetch_tensormap(&p.mv);
   }
   if (warp == 1) tmem_alloc_pair(&tmem_slot, kTmemCols);
 
@@ -308,6 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- output
     const int half = (warp - 4) >> 2, quad = warp & 3;  // 0: keys, 1: values
+    const uint64_t once = l2_policy_evict_first();
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     uint16_t* const base = half ? a.v : a.k;
     uint32_t d = 0, dp = 0;
@@ -326,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
       if (!__all_sync(~0u, mbar_wait_bounded(&d_full[d], dp, a.dev_status))) break;
       tc_fence_after();
       const uint32_t col = tmem + lanes + d * 256u + (uint32_t)half * 128u;
-      uint8_t* stage = smem + lay.out + (uint32_t)(warp - 4) * kOutWarp;
+      uint8_t* stage = smem + lay.out + (uint32_t)((warp - 4) * p.out_rows) * 128;
       const int row0 = u.j * kRows + quad * 32, piece = lane & 7;
       uint16_t* out = base + ((size_t)(u.s0 + row0) * a.H + u.h) * 128 + piece * 8;
 #pragma unroll 1
@@ -335,23 +341,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
         tmem_ld32(col + c, x[0]);
         tmem_ld32(col + c + 32, x[1]);
         tmem_wait_ld();
+        for (int part = 0; part < 32; part += p.out_rows) {
+          bulk_wait_read_all();  // (of the lane that stores; the others have no group)
+          __syncwarp();
+          if ((unsigned)(lane - part) < (unsigned)p.out_rows) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 8) {  // a row's 16-byte pieces are rotated by its number
-          uint4 y;
-          y.x = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31)]), __uint_as_float(x[e >> 5][(e & 31) + 1]));
-          y.y = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 2]), __uint_as_float(x[e >> 5][(e & 31) + 3]));
-          y.z = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 4]), __uint_as_float(x[e >> 5][(e & 31) + 5]));
-          y.w = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 6]), __uint_as_float(x[e >> 5][(e & 31) + 7]));
-          *reinterpret_cast<uint4*>(stage + lane * 128 + (((e >> 3) ^ (lane & 7)) << 4)) = y;
+            for (int e = 0; e < 64; e += 8) {  // in the 128-byte swizzle: a row's 16-byte pieces are rotated by its number
+              uint4 y;
+              y.x = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31)]), __uint_as_float(x[e >> 5][(e & 31) + 1]));
+              y.y = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 2]), __uint_as_float(x[e >> 5][(e & 31) + 3]));
+              y.z = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 4]), __uint_as_float(x[e >> 5][(e & 31) + 5]));
+              y.w = pack_bf16x2_rn(__uint_as_float(x[e >> 5][(e & 31) + 6]), __uint_as_float(x[e >> 5][(e & 31) + 7]));
+              *reinterpret_cast<uint4*>(stage + (lane - part) * 128 + (((e >> 3) ^ (lane & 7)) << 4)) = y;
+            }
+          }
+          if (row0 + part + p.out_rows <= u.len) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(half ? &p.mv : &p.mk, stage, c, u.h, u.s0 + row0 + part, once);
+              bulk_commit();
+            }
+          } else {  // (the sequence ends inside: its rows only)
+            __syncwarp();
+            for (int r = lane >> 3; r < p.out_rows; r += 4) {
+              const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+              if (row0 + part + r < u.len)
+                __stcs(reinterpret_cast<uint4*>(out + (size_t)(part + r) * a.H * 128 + c), y);
+            }
+          }
         }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3);
-          const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
-          if (row0 + r < u.len) __stcs(reinterpret_cast<uint4*>(out + (size_t)r * a.H * 128 + c), y);
-        }
-        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -359,6 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
       d ^= 1u;
       if (d == 0) dp ^= 1u;
     }
+    bulk_wait_read_all();  // (shared memory stays until the copies have read it)
   }
   __syncwarp();
   tc_fence_before();
@@ -379,16 +399,22 @@ cudaError_t launch_shared_expand(const SharedExpandArgs& a, cudaStream_t stream)
   // two row tiles where at least three weight chunks fit beside them
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
   p.nb = 3;
-  p.na = layout_of(p.chunks, 2, p.nb).total <= kMost ? 2 : 1;
-  while (p.nb < kMaxStages && layout_of(p.chunks, p.na, p.nb + 1).total <= kMost) ++p.nb;
-  uint32_t smem = layout_of(p.chunks, p.na, p.nb).total;
+  p.out_rows = 32;
+  p.na = layout_of(p.chunks, 2, p.nb, 32).total <= kMost ? 2 : 1;
+  while (p.nb < kMaxStages && layout_of(p.chunks, p.na, p.nb + 1, 32).total <= kMost) ++p.nb;
+  // With one row tile in 128 KB the ring is short, and another chunk is worth more than whole stores
+  // (128 heads at r 512: 116 us against 123); with two it is not (r 256: 27.0 us against 23.5).
+  if (p.na == 1 && p.nb < kMaxStages && layout_of(p.chunks, 1, p.nb + 1, 16).total <= kMost) ++p.nb, p.out_rows = 16;
+  uint32_t smem = layout_of(p.chunks, p.na, p.nb, p.out_rows).total;
   if (smem > kMost) return cudaErrorInvalidValue;
   if (smem < 120u * 1024u) smem = 120u * 1024u;  // one CTA an SM: it holds all of TMEM
   const uint64_t w = (uint64_t)(a.r + a.dr), r = (uint64_t)a.r;
   if (!encode_tiled_bf16_2d(&p.mc, a.pages, w, (uint64_t)a.num_pages * a.page_size, w * 2, 64, 64,
                             CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tiled_bf16_2d(&p.mwk, a.W_K, r, (uint64_t)a.H * 128, r * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tiled_bf16_2d(&p.mwv, a.W_V, r, (uint64_t)a.H * 128, r * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+      !encode_tiled_bf16_2d(&p.mwv, a.W_V, r, (uint64_t)a.H * 128, r * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_bf16_3d(&p.mk, a.k, {128, (uint64_t)a.H, (uint64_t)a.N}, {256, (uint64_t)a.H * 256}, {64, 1, (uint32_t)p.out_rows}) ||
+      !encode_tiled_bf16_3d(&p.mv, a.v, {128, (uint64_t)a.H, (uint64_t)a.N}, {256, (uint64_t)a.H * 256}, {64, 1, (uint32_t)p.out_rows}))
     return cudaErrorInvalidValue;
   static SmemLimit limit;
   cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_shared_expand_kernel), a.device, (int)smem);

@@ -87,6 +87,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
       : "memory");
 }
 
+// A box from shared memory, to be committed to a bulk group.
+__device__ __forceinline__ void tma_store_3d(const void* map, const void* src, int x, int y, int z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(map),
+      "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "l"(policy)
+      : "memory");
+}
+
 // mbar_wait_bounded for barriers that are mostly complete already.
 __device__ __forceinline__ bool mbar_wait_ready(uint64_t* bar, uint32_t parity, uint32_t* dev_status) {
   return mbar_test(bar, parity) || mbar_wait_bounded(bar, parity, dev_status);
