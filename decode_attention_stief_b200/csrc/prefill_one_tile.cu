@@ -1,6 +1,6 @@
 // prefill_one_tile.cu -- causal attention of ragged prompts over per-head keys and values, for sm_100a:
-// two CTAs an SM, a tile of 128 query rows each (prefill_attention.cu has the formula, the form with
-// two tiles a CTA, and the rule between them).
+// two CTAs an SM, a tile of 128 query rows each (prefill_attention.cu has the formula, the form in
+// which two CTAs share the keys, and the rule between them).
 //
 // A CTA walks the keys in steps of 64; both products run on tcgen05:
 //     S [128 x 64] = Q . K^T,    O [128 x 128] += P . V,
@@ -26,9 +26,8 @@
 // anew) and its copies write 32: 768 cycles at 128 bytes a cycle, where the products alone would take
 // 512 and the exponentials, 16 a cycle on an SM, another 512 beside them.  Of the some 1900 cycles that
 // a step of both CTAs takes that is 80 %; the tensor cores are busy for 47 % (chunks) of the time.
-// (Two tiles of queries that share the keys read and write a third less, but their CTA has an SM to
-// itself and no second buffer of scores: 8 chunks of 512 over 3012 keys 208 us against 238, but 2500
-// tokens 69 against 57.5, and 8 chunks of 128 over 4128 keys 134 against 89.)
+// (Pairs of CTAs, each with half of the keys and values, ask less of it: 8 chunks of 512 over 3012 keys
+// 216 us against 239; but 2500 tokens 66 against 58, and 8192, 32 heads over 8, 456 both.)
 // Measured: 8192 tokens, 32 heads over 8: 456 us, 1.21 PFLOP/s; 8 prompts of 65 to 1500: 84.9 us,
 // 0.74 PFLOP/s (its diagonal tiles compute twice what is counted); 5 prompts of up to 64: 5.7 us.
 #include <cstdint>

@@ -87,6 +87,48 @@ def test_prefill_peaked_and_flat_scores(scale):
     _check(got, q, k, v, pe, [0, 400], [0, 400], scale)
 
 
+@pytest.mark.parametrize("Hq,Hkv,dr", [(1, 1, 64), (4, 2, 64), (8, 1, 16), (5, 5, 48), (6, 2, 32), (256, 1, 16)])
+@pytest.mark.parametrize("nq,nk", [([1], [1]), ([77], [77]), ([128, 129, 1], [128, 129, 1]), ([300], [555]),
+                                   ([5, 0, 64, 1], [200, 3, 64, 0]), ([260, 40], [100, 39]), ([513], [513]),
+                                   ([257, 31, 383], [321, 1031, 2000])])
+def test_prefill_within_long_arrays(nq, nk, Hq, Hkv, dr):
+    """The same kinds of batches at the head of arrays of many more rows (a padded batch), which hold
+    NaN there: a long walk over the keys is expected, and CTAs work in pairs."""
+    q, k, v, pe = _inputs(nq, nk, Hq, Hkv, dr, sum(nq) + dr, pad=9)
+    more = 1024 * len(nk)
+    k, v, pe = (torch.cat([x, torch.full((more, *x.shape[1:]), float("nan"), dtype=x.dtype, device=DEV)])
+                for x in (k, v, pe))
+    qs, ks = _starts(nq, 4), _starts(nk, 3)
+    for x, s in ((q, qs), (k, ks), (v, ks), (pe, ks)):
+        x[: s[0]] = float("nan")
+        x[s[-1]:] = float("nan")
+    scale = 1.5 / (128 + dr) ** 0.5
+    got = _prefill(q, k, v, pe, qs, ks, max(nq), scale)
+    _check(got, q, k, v, pe, qs, ks, scale)
+    assert torch.all(got[: qs[0]] == 7.0) and torch.all(got[qs[-1]:] == 7.0)
+
+
+@pytest.mark.parametrize("scale", [1.0, -0.5, 0.0])
+def test_prefill_late_peaks_over_a_long_walk(scale):
+    q, k, v, pe = _inputs([400], [1400], 4, 4, 64, 79)
+    k *= torch.linspace(0.2, 4.0, 1400, device=DEV)[:, None, None].to(torch.bfloat16)
+    k[:, :, 0] = torch.linspace(0.0, 9.0, 1400, device=DEV)[:, None].to(torch.bfloat16) * (1 if scale > 0 else -1)
+    q[:, :, 0] = 20.0
+    got = _prefill(q, k, v, pe, [0, 400], [0, 1400], 400, scale)
+    _check(got, q, k, v, pe, [0, 400], [0, 1400], scale)
+
+
+def test_prefill_bad_rows_over_a_long_walk():
+    q, k, v, pe = _inputs([50, 50], [1160, 1160], 2, 2, 16, 5)
+    good = _prefill(q, k, v, pe, [0, 50, 100], [0, 1160, 2320], 50, 0.1)
+    for qs, ks, most in (([0, 50, 101], [0, 1160, 2320], 60), ([0, 50, 100], [0, 1160, 2321], 50),
+                         ([0, 50, 40], [0, 1160, 2320], 50), ([0, 50, 100], [0, 1160, 1159], 50)):
+        got = _prefill(q, k, v, pe, qs, ks, most, 0.1, expect=stief.DEV_BAD_LENGTH)
+        assert torch.equal(got[:50], good[:50]) and torch.all(got[50:] == 7.0)
+    for _ in range(20):  # the same every time
+        assert torch.equal(_prefill(q, k, v, pe, [0, 50, 100], [0, 1160, 2320], 50, 0.1), good)
+
+
 @pytest.mark.parametrize("scale", [1.0, -0.5])
 @pytest.mark.parametrize("nq,dr", [(400, 0), (30, 16), (400, 16)])
 def test_prefill_late_peaks(nq, dr, scale):
