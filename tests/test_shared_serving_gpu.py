@@ -197,3 +197,34 @@ def test_shared_pages_and_one_query_prompts():
             kk, vv = (x.repeat_interleave(4, 1).transpose(0, 1) for x in (kk, v[ks[b]: ks[b + 1]].double()))
             want, bound = attention(q[b: b + 1].double().transpose(0, 1), kk, vv, 0.1)
             check(out[b][:, None], want, bound)
+
+
+def test_paired_prompts_beside_single_tiles():
+    """Prompts whose CTAs work in pairs and prompts whose CTAs do not, on streams of their own: an SM
+    of a pair may hold another kernel's CTA where its neighbour holds none."""
+    gen = torch.Generator().manual_seed(12)
+    # (queries, keys, heads, KV heads, position values); more than 1024 keys with positions: pairs
+    shapes = [(1500, 1500, 4, 4, 64), (300, 100, 3, 1, 0), (1100, 2100, 5, 5, 16), (700, 900, 7, 7, 0),
+              (129, 5000, 37, 1, 64), (90, 90, 29, 29, 16)]
+    runs = []
+    for nq, nk, Hq, Hkv, dr in shapes:
+        t = [bf(*s, gen=gen).to(DEV) for s in ((nq, Hq, 128 + dr), (nk, Hkv, 128), (nk, Hkv, 128), (nk, dr))]
+        runs.append((t, _i([0, nq]), _i([0, nk]), nq, _empty(nq, Hq, 128), _i([0])))
+
+    def call(t, qs, ks, nq, out, status):
+        stief.stief_prefill_attention(t[0], t[1], t[2], qs, ks, out, nq, 0.08, k_pe=t[3] if t[3].shape[1] else None,
+                                      dev_status=status)
+
+    for run in runs:
+        call(*run)
+    torch.cuda.synchronize()
+    want = [run[4].clone() for run in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    for n in range(40):
+        for i, (s, run) in enumerate(zip(streams, runs)):
+            with torch.cuda.stream(s):
+                for _ in range(1 + (n + i) % 3):
+                    call(*run)
+    torch.cuda.synchronize()
+    for run, x in zip(runs, want):
+        assert int(run[5].item()) == 0 and torch.equal(run[4], x)
