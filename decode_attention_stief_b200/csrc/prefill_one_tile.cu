@@ -16,6 +16,10 @@
 // With a position part a query row is 192 columns and one slot of keys fits instead of two: the
 // slot whose successor is needed latest, because scores are computed a step ahead (two slots of keys
 // and one of values: 1 chunk of 128 over 8128 keys, 128 heads, 200 us; this way 182).
+// Where tiles are few and walks long (split_of in prefill_attention.cu), the CTAs of a cluster share a
+// tile's keys: each walks its part, leaves its rows of O, m and l in fp32 in its shared memory, and
+// joins its share of the rows from all of them.  1 query over 8001 keys, 8 heads over 1: 15.5 us
+// against 82; over 32001: 45 against 313; 8 chunks of 17 over 989, 4 heads: 9.2 against 14.9.
 //   warp 0: TMA producer; warp 1: MMA issuer; warp 2: zeroes the value rows past n_k in the last step
 //   (they may hold NaN, and 0 * NaN is NaN); warps 4-7: softmax, a thread a row, and the output.
 // The softmax's reference is the first step's maximum of the row and moves only when a score passes
@@ -49,6 +53,7 @@ constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kOCol = 128;            // S at 0 and 64, O at 128
 constexpr float kRescale = 60.f;           // log2 units a score may pass the reference by
 constexpr float kFloor = -1e30f;
+constexpr int kMaxSplit = 8;                // a cluster of any GPU
 
 struct Args {
   CUtensorMap mq;   // q [Nq][Hq][128], box 64 columns x pack heads x 128 / pack queries
@@ -59,6 +64,7 @@ struct Args {
   int pack;         // heads of a tile: its row r is query r / pack, head r % pack (pack divides 128)
   int shift;        // log2(pack)
   int qtiles;       // tiles of the longest sequence
+  int split;        // CTAs (a cluster) that share a tile's keys: 1, 2, 4 or 8
   float scale2;     // |scale| * log2(e)
   int negate;       // scale < 0: the products are negated instead
 #ifdef STIEF_TEST_HOOKS
@@ -75,10 +81,14 @@ struct Form {
   static constexpr uint32_t kTotal = kBars + 8 * 20;
 };
 static_assert(2 * (Form<true>::kTotal + 1024) <= 228 * 1024, "two CTAs share an SM");
+// The parts of a split tile: its rows of O in fp32, then (m, l) of each, over what the queries, keys
+// and values took.
+constexpr uint32_t kPartRow = 512, kPartMl = kRows * kPartRow;
+static_assert(kPartMl + kRows * 8 <= Form<false>::kBars, "the parts fit");
 
 }  // namespace
 
-template <bool kPe>
+template <bool kPe, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(const __grid_constant__ Args p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using F = Form<kPe>;
@@ -117,23 +127,34 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
     for (int i = 14; i < 19; ++i) mbar_init(&k_full[i], 1);
     fence_barrier_init();
   }
-  const int groups = a.Hq >> p.shift, gb = groups * a.B, rest = (int)(blockIdx.x % (unsigned)gb);
-  const int qt = p.qtiles - 1 - (int)(blockIdx.x / (unsigned)gb);
+  const unsigned tile = kSplit ? blockIdx.x / (unsigned)p.split : blockIdx.x;
+  const int rank = kSplit ? (int)cluster_rank() : 0;
+  const int groups = a.Hq >> p.shift, gb = groups * a.B, rest = (int)(tile % (unsigned)gb);
+  const int qt = p.qtiles - 1 - (int)(tile / (unsigned)gb);
   const int b = rest / groups, h0 = (rest % groups) << p.shift, hk = h0 / (a.Hq / a.Hkv);
 
   pdl_wait();
   const int q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1);
-  const int k0 = __ldg(a.kv_start + b), k1 = __ldg(a.kv_start + b + 1);
+  int k0 = __ldg(a.kv_start + b);
+  const int k1 = __ldg(a.kv_start + b + 1);
   if (q0 < 0 || q1 < q0 || q1 > a.Nq || k0 < 0 || k1 < k0 || k1 > a.Nkv || q1 - q0 > a.max_q) {
-    if (tid == 0 && h0 == 0 && qt == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
+    if (tid == 0 && rank == 0 && h0 == 0 && qt == 0) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
     return;
   }
-  const int nq = q1 - q0, n_k = k1 - k0, first = qt * (kRows >> p.shift);  // first query
+  const int nq = q1 - q0, n_all = k1 - k0, first = qt * (kRows >> p.shift);  // first query
   if (first >= nq) return;
   // steps of keys that the tile's last query sees
   const int last = min(nq, first + (kRows >> p.shift)) - 1;
-  const long long most = (long long)last + n_k - nq + 1;
-  const int n = most > 0 ? (int)((min(most, (long long)n_k) + kKeys - 1) / kKeys) : 0;
+  const long long most = (long long)last + n_all - nq + 1;
+  int n = most > 0 ? (int)((min(most, (long long)n_all) + kKeys - 1) / kKeys) : 0;
+  int n_k = n_all, before = 0;  // keys from k0 on, and those of the CTAs before this one
+  if (kSplit) {
+    const int per = (n + p.split - 1) / p.split, js = min(n, rank * per);
+    n = min(per, n - js);
+    before = js * kKeys;
+    k0 += before;
+    n_k = min(n_all - before, n * kKeys);
+  }
 
   // (only after the dependency wait, and before this kernel's own dependents may start: a CTA that
   // holds tensor memory while it waits for another kernel must not starve one of that kernel's)
@@ -260,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
     const int quad = warp & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16, o_col = tmem + lanes + kOCol;
     const int r0 = quad * 32, query = first + ((r0 + lane) >> p.shift);  // the thread's row
-    const int seen = (int)max(0LL, min((long long)n_k, (long long)query + n_k - nq + 1));  // keys it sees
+    const int sees = (int)max(0LL, min((long long)n_all, (long long)query + n_all - nq + 1));  // keys it sees
+    const int seen = sees - before;  // (at or below 0: none of this CTA's)
     const int all = __shfl_sync(~0u, seen, 0);  // keys that every row of the warp sees
     const uint64_t scale2 = pack2(p.scale2, p.scale2);
     float m = kFloor;
@@ -344,7 +366,25 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
     }
     // the output: zeros for a row that sees no key
     if (ok && n > 0) ok = __all_sync(~0u, mbar_wait_ready(o_full, 0, a.dev_status));
-    if (ok) {
+    if (kSplit && ok) {
+      // this CTA's part; a row's 16-byte pieces are rotated by its number
+      tc_fence_after();
+      const uint64_t ls = add2(l0, l1);
+      uint8_t* part = smem + (uint32_t)(r0 + lane) * kPartRow;
+      *reinterpret_cast<float2*>(smem + kPartMl + (uint32_t)(r0 + lane) * 8) = make_float2(m, lo_of(ls) + hi_of(ls));
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t v[32] = {};
+        if (n > 0) {
+          tmem_ld32(o_col + c, v);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<uint4*>(part + ((((c + e) >> 2) ^ lane) << 4)) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      }
+    }
+    if (!kSplit && ok) {
       tc_fence_after();
       const uint64_t ls = add2(l0, l1);
       const float inv = seen > 0 ? 1.f / (lo_of(ls) + hi_of(ls)) : 0.f;
@@ -382,20 +422,59 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if (kSplit) cluster_sync();  // every CTA's part is in its shared memory
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  if (kSplit) {
+    // each CTA joins its share of the rows, a warp a row
+    const int rows = kRows / p.split;
+    for (int i = warp; i < rows; i += kThreads / 32) {
+      const int r = rank * rows + i, query = first + (r >> p.shift), h = h0 + (r & (p.pack - 1));
+      if (query >= nq) break;
+      float2 ml[kMaxSplit];
+      float4 o[kMaxSplit];
+#pragma unroll
+      for (int k = 0; k < kMaxSplit; ++k)
+        if (k < p.split) {
+          const uint32_t at = in_cta(smem, (uint32_t)k);
+          ml[k] = load_cluster_f2(at + kPartMl + (uint32_t)r * 8);
+          o[k] = load_cluster_f4(at + (uint32_t)r * kPartRow + (uint32_t)((lane ^ (r & 31)) << 4));
+        }
+      float top = kFloor, l = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxSplit; ++k)
+        if (k < p.split && ml[k].y > 0.f) top = fmaxf(top, ml[k].x);
+#pragma unroll
+      for (int k = 0; k < kMaxSplit; ++k)
+        if (k < p.split && ml[k].y > 0.f) {
+          const float f = fast_exp2(ml[k].x - top);
+          l += f * ml[k].y;
+          x.x += f * o[k].x;
+          x.y += f * o[k].y;
+          x.z += f * o[k].z;
+          x.w += f * o[k].w;
+        }
+      const float inv = l > 0.f ? 1.f / l : 0.f;  // (zeros for a row that sees no key)
+      *reinterpret_cast<uint2*>(a.out + ((size_t)(q0 + query) * a.Hq + h) * 128 + lane * 4) =
+          make_uint2(pack_bf16x2_rn(x.x * inv, x.y * inv), pack_bf16x2_rn(x.z * inv, x.w * inv));
+    }
+    __syncwarp();
+    cluster_sync();  // no part is read any more
   }
 }
 
 namespace {
 
-template <bool kPe>
-cudaError_t launch(const PrefillArgs& a, int pack, cudaStream_t stream) {
+template <bool kPe, bool kSplit>
+cudaError_t launch(const PrefillArgs& a, int pack, int split, cudaStream_t stream) {
   Args p{};
   p.a = a;
   p.pack = pack;
+  p.split = split;
   while ((1 << p.shift) < p.pack) ++p.shift;
   const int queries = kRows / p.pack;
   p.qtiles = (int)((a.max_q + (long long)queries - 1) / queries);
@@ -405,7 +484,7 @@ cudaError_t launch(const PrefillArgs& a, int pack, cudaStream_t stream) {
 #ifdef STIEF_TEST_HOOKS
   p.stall = test_stall_bytes();
 #endif
-  const long long blocks = (long long)p.qtiles * (a.Hq / p.pack) * a.B;
+  const long long blocks = (long long)p.qtiles * (a.Hq / p.pack) * a.B * split;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const uint64_t rows = a.Nkv > 0 ? a.Nkv : 1, dk = (uint64_t)a.Hkv * 128;  // (no keys: the maps are never used)
   const int dq = 128 + a.dr;
@@ -419,25 +498,29 @@ cudaError_t launch(const PrefillArgs& a, int pack, cudaStream_t stream) {
                                     CU_TENSOR_MAP_SWIZZLE_128B)))
     return cudaErrorInvalidValue;
   static SmemLimit limit;
-  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_prefill_one_tile_kernel<kPe>), a.device, (int)Form<kPe>::kTotal);
+  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(stief_prefill_one_tile_kernel<kPe, kSplit>), a.device, (int)Form<kPe>::kTotal);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Form<kPe>::kTotal;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, stief_prefill_one_tile_kernel<kPe>, p);
+  cfg.numAttrs = kSplit ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, stief_prefill_one_tile_kernel<kPe, kSplit>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_prefill_one_tile(const PrefillArgs& a, int pack, cudaStream_t stream) {
-  return a.dr > 0 ? launch<true>(a, pack, stream) : launch<false>(a, pack, stream);
+cudaError_t launch_prefill_one_tile(const PrefillArgs& a, int pack, int split, cudaStream_t stream) {
+  if (split > 1) return a.dr > 0 ? launch<true, true>(a, pack, split, stream) : launch<false, true>(a, pack, split, stream);
+  return a.dr > 0 ? launch<true, false>(a, pack, 1, stream) : launch<false, false>(a, pack, 1, stream);
 }
 
 }  // namespace stief

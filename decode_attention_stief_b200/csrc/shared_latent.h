@@ -83,6 +83,6 @@ struct PrefillArgs {
   int device, sms;
 };
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
-cudaError_t launch_prefill_one_tile(const PrefillArgs& a, int pack, cudaStream_t stream);
+cudaError_t launch_prefill_one_tile(const PrefillArgs& a, int pack, int split, cudaStream_t stream);
 
 }  // namespace stief

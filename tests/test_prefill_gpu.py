@@ -129,6 +129,87 @@ def test_prefill_bad_rows_over_a_long_walk():
         assert torch.equal(_prefill(q, k, v, pe, [0, 50, 100], [0, 1160, 2320], 50, 0.1), good)
 
 
+@pytest.mark.parametrize("nq,nk,Hq,Hkv", [
+    ([1], [1037], 4, 4), ([3], [5000], 8, 1), ([900], [600], 1, 1), ([1, 1, 1], [5000, 3, 0], 4, 2),       # eight CTAs a tile
+    ([130], [8250], 24, 24), ([17, 0, 90], [2000, 700, 1100], 6, 6), ([513], [513], 3, 3),
+    ([200, 130], [1300, 1100], 8, 8), ([64] * 6, [640 + 77 * i for i in range(6)], 20, 5), ([70, 450], [64, 1090], 5, 5),  # four
+    ([300], [1100], 40, 40), ([260, 40], [2100, 39], 76, 38)])                                             # two
+@pytest.mark.parametrize("dr", [0, 16, 64])
+def test_prefill_keys_split_over_ctas(nq, nk, Hq, Hkv, dr):
+    """Few tiles of queries and long walks; rows of no sequence hold NaN, and some queries, or some of
+    the CTAs of a tile, see no key."""
+    q, k, v, pe = _inputs(nq, nk, Hq, Hkv, dr, sum(nk) + dr, pad=9)
+    qs, ks = _starts(nq, 4), _starts(nk, 3)
+    for x, s in ((q, qs), (k, ks), (v, ks), (pe, ks)):
+        x[: s[0]] = float("nan")
+        x[s[-1]:] = float("nan")
+    scale = 1.5 / (128 + dr) ** 0.5
+    got = _prefill(q, k, v, pe, qs, ks, max(nq), scale)
+    _check(got, q, k, v, pe, qs, ks, scale)
+    assert torch.all(got[: qs[0]] == 7.0) and torch.all(got[qs[-1]:] == 7.0)
+    for _ in range(5):  # the same every time
+        again = _prefill(q, k, v, pe, qs, ks, max(nq), scale)
+        assert torch.equal(again[qs[0]: qs[-1]], got[qs[0]: qs[-1]])
+
+
+@pytest.mark.parametrize("nq", [2, 150])
+@pytest.mark.parametrize("at", [0, 1000, 2399])
+def test_prefill_one_key_outweighs_a_split_walk(nq, at):
+    """All the weight lies in the keys of one of a tile's CTAs, the others' parts vanish."""
+    q, k, v, pe = _inputs([nq], [2400 + nq], 4, 4, 16, at + nq)
+    q[:, :, 0], k[:, :, 0] = 30.0, 0.0
+    k[at, :, 0] = 40.0
+    got = _prefill(q, k, v, pe, [0, nq], [0, 2400 + nq], nq, 1.0)
+    _check(got, q, k, v, pe, [0, nq], [0, 2400 + nq], 1.0)
+    assert torch.equal(got, v[at].expand(nq, 4, 128))
+
+
+@pytest.mark.parametrize("Hq,Hkv,dr", [(40, 40, 64), (160, 40, 48), (96, 48, 16)])
+@pytest.mark.parametrize("nq,nk", [([257, 31, 383], [321, 1031, 2000]), ([300, 200], [555, 100]), ([513], [513])])
+def test_prefill_many_heads_within_long_arrays(nq, nk, Hq, Hkv, dr):
+    """As many tiles as keep the GPU busy, and a long walk expected: CTAs in pairs."""
+    q, k, v, pe = _inputs(nq, nk, Hq, Hkv, dr, sum(nq) + dr, pad=9)
+    more = 1024 * len(nk)
+    k, v, pe = (torch.cat([x, torch.full((more, *x.shape[1:]), float("nan"), dtype=x.dtype, device=DEV)])
+                for x in (k, v, pe))
+    qs, ks = _starts(nq, 4), _starts(nk, 3)
+    for x, s in ((q, qs), (k, ks), (v, ks), (pe, ks)):
+        x[: s[0]] = float("nan")
+        x[s[-1]:] = float("nan")
+    scale = 1.5 / (128 + dr) ** 0.5
+    got = _prefill(q, k, v, pe, qs, ks, max(nq), scale)
+    _check(got, q, k, v, pe, qs, ks, scale)
+    assert torch.all(got[: qs[0]] == 7.0) and torch.all(got[qs[-1]:] == 7.0)
+    for _ in range(5):
+        again = _prefill(q, k, v, pe, qs, ks, max(nq), scale)
+        assert torch.equal(again[qs[0]: qs[-1]], got[qs[0]: qs[-1]])
+
+
+@pytest.mark.parametrize("scale", [1.0, -0.5, 0.0])
+def test_prefill_many_heads_late_peaks(scale):
+    q, k, v, pe = _inputs([400], [1400], 40, 40, 64, 80)
+    k *= torch.linspace(0.2, 4.0, 1400, device=DEV)[:, None, None].to(torch.bfloat16)
+    k[:, :, 0] = torch.linspace(0.0, 9.0, 1400, device=DEV)[:, None].to(torch.bfloat16) * (1 if scale > 0 else -1)
+    q[:, :, 0] = 20.0
+    got = _prefill(q, k, v, pe, [0, 400], [0, 1400], 400, scale)
+    _check(got, q, k, v, pe, [0, 400], [0, 1400], scale)
+
+
+def test_prefill_split_captured_with_new_lengths():
+    """A graph captured for a long walk, replayed with shorter ones: some CTAs of a tile get nothing."""
+    q, k, v, pe = _inputs([60], [3000], 4, 4, 64, 19)
+    qs, ks, out = _i([0, 60]), _i([0, 3000]), torch.zeros((60, 4, 128), dtype=torch.bfloat16, device=DEV)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        stief.stief_prefill_attention(q, k, v, qs, ks, out, 60, 0.1, k_pe=pe)
+    for n, m in ((60, 3000), (31, 700), (1, 65), (60, 40), (2, 1), (7, 0)):
+        qs.copy_(_i([0, n]))
+        ks.copy_(_i([0, m]))
+        graph.replay()
+        torch.cuda.synchronize()
+        _check(out, q, k, v, pe, [0, n], [0, m], 0.1)
+
+
 @pytest.mark.parametrize("scale", [1.0, -0.5])
 @pytest.mark.parametrize("nq,dr", [(400, 0), (30, 16), (400, 16)])
 def test_prefill_late_peaks(nq, dr, scale):

@@ -200,12 +200,13 @@ def test_shared_pages_and_one_query_prompts():
 
 
 def test_paired_prompts_beside_single_tiles():
-    """Prompts whose CTAs work in pairs and prompts whose CTAs do not, on streams of their own: an SM
-    of a pair may hold another kernel's CTA where its neighbour holds none."""
+    """Prompts whose CTAs work in pairs, prompts whose CTAs do not, and some whose CTAs share a tile's
+    keys, on streams of their own: an SM of a pair may hold another kernel's CTA where its neighbour
+    holds none."""
     gen = torch.Generator().manual_seed(12)
-    # (queries, keys, heads, KV heads, position values); more than 1024 keys with positions: pairs
+    # (queries, keys, heads, KV heads, position values); the last two work in pairs
     shapes = [(1500, 1500, 4, 4, 64), (300, 100, 3, 1, 0), (1100, 2100, 5, 5, 16), (700, 900, 7, 7, 0),
-              (129, 5000, 37, 1, 64), (90, 90, 29, 29, 16)]
+              (129, 5000, 37, 1, 64), (90, 90, 29, 29, 16), (700, 1300, 40, 40, 64), (200, 2100, 150, 75, 16)]
     runs = []
     for nq, nk, Hq, Hkv, dr in shapes:
         t = [bf(*s, gen=gen).to(DEV) for s in ((nq, Hq, 128 + dr), (nk, Hkv, 128), (nk, Hkv, 128), (nk, dr))]

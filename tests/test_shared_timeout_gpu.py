@@ -95,5 +95,13 @@ def test_prefill_over_a_long_walk(hooks):
                         _i([0]), [out], k_pe=pe)
 
 
+def test_prefill_pairs(hooks):
+    gen = torch.Generator().manual_seed(6)
+    q, k, v = (bf(*s, gen=gen).to(DEV) for s in ((600, 40, 192), (1400, 40, 128), (1400, 40, 128)))
+    pe, out = bf(1400, 64, gen=gen).to(DEV), torch.zeros((600, 40, 128), dtype=torch.bfloat16, device=DEV)
+    _stalled_then_right(hooks, stief.stief_prefill_attention, (q, k, v, _i([0, 600]), _i([0, 1400]), out, 600, 0.1),
+                        _i([0]), [out], k_pe=pe)
+
+
 def test_library_is_the_one_of_the_binding():
     assert _binding.library_path() != stief_build.library_file("testhooks")
