@@ -723,19 +723,18 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
 }
 
 // Joins the partial states of sequences that several CTAs hold, and writes the zeros of empty
-// ones.  A warp takes 512 dims of a head (kWarps = 1), or, where few sequences have many parts
-// each, a CTA takes 128 dims of a head and its warps share the parts.  Bound by latency: the
-// lengths and the meta word are read together, then everything else of up to kBatch parts.
-template <int kWarps>
+// ones.  kWarps warps share a head's parts (a CTA has one head, or eight if kWarps = 1), and a warp
+// holds kVec chunks of 128 dims.  Bound by latency: the lengths and the meta word are read together,
+// then everything else of up to kBatch parts.
+template <int kWarps, int kVec>
 __global__ void __launch_bounds__(kWarps == 1 ? 256 : 32 * kWarps) stief_shared_merge_kernel(const SharedDecodeArgs a, int NH, int groups, int G) {
-  constexpr int kVec = kWarps == 1 ? 4 : 1;     // 128-dim chunks a warp holds
-  constexpr int kBatch = kWarps == 1 ? 2 : 8;   // parts in flight
-  __shared__ float4 acc_s[kWarps][32];
+  constexpr int kBatch = kVec == 4 ? 2 : 8;  // parts in flight
+  __shared__ float4 acc_s[kWarps][kVec][32];
   __shared__ float2 ml_s[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
   const int nd = (a.r + 127) / 128;
-  const int h = kWarps == 1 ? (int)blockIdx.x * 8 + warp : (int)blockIdx.x / nd;
-  const int d0 = (kWarps == 1 ? 0 : (int)blockIdx.x % nd * 128) + lane * 4;
+  const int h = kWarps == 1 ? (int)blockIdx.x * 8 + warp : kVec == 4 ? (int)blockIdx.x : (int)blockIdx.x / nd;
+  const int d0 = (kVec == 4 ? 0 : (int)blockIdx.x % nd * 128) + lane * 4;
   uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
   pdl_wait();
   pdl_launch_dependents();
@@ -800,22 +799,27 @@ __global__ void __launch_bounds__(kWarps == 1 ? 256 : 32 * kWarps) stief_shared_
     }
   }
   if (kWarps > 1) {
-    acc_s[warp][lane] = acc[0];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) acc_s[warp][j][lane] = acc[j];
     if (lane == 0) ml_s[warp] = make_float2(M, l);
     __syncthreads();
-    if (warp != 0) return;
-    for (int k = 1; k < kWarps; ++k) M = fmaxf(M, ml_s[k].x);
+    if (warp >= kVec) return;  // a warp a chunk joins the warps
+    for (int k = 0; k < kWarps; ++k) M = k == 0 ? ml_s[0].x : fmaxf(M, ml_s[k].x);
     l = 0.f;
-    acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < kWarps; ++k) {
       const float f = fast_exp2(ml_s[k].x - M);
-      const float4 o = acc_s[k][lane];
+      const float4 o = acc_s[k][warp][lane];
       l += f * ml_s[k].y;
-      acc[0].x += f * o.x;
-      acc[0].y += f * o.y;
-      acc[0].z += f * o.z;
-      acc[0].w += f * o.w;
+      x.x += f * o.x;
+      x.y += f * o.y;
+      x.z += f * o.z;
+      x.w += f * o.w;
     }
+    const float inv = 1.f / l;
+    if (d0 + 128 * warp < a.r)
+      *reinterpret_cast<uint2*>(out + 128 * warp) = make_uint2(pack_bf16x2_rn(x.x * inv, x.y * inv), pack_bf16x2_rn(x.z * inv, x.w * inv));
+    return;
   }
   const float inv = 1.f / l;
 #pragma unroll
@@ -896,18 +900,32 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess || p.whole) return e;
-  cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  // Few sequences, hence many parts each: the warps of a CTA share them, where one wave of such CTAs
-  // holds the whole output; else a warp a head.  (5 sequences of 1024 tokens: 8.7 against 10.5 us
-  // with 16 heads at rank 128; with 64 at rank 512, five waves, 24.9 against 15.2.)
-  if (p.G > 8 * a.B && (long long)a.Hq * p.nm * a.B <= 4LL * a.sms) {
+  // The warps of a CTA share a head's parts, whose number only the GPU knows: sixteen where a
+  // sequence may have very many (and one wave holds the output), four otherwise, 128 dims a CTA
+  // where sequences are few and the CTAs too, else all dims; with too many CTAs even so, a warp a
+  // head.  (In us, a warp a head, 4 warps with 512 dims, 4 with 128, 16: 1 sequence of 32768, 32 heads,
+  // 55.4, 30.1, 23.2, 19.7; 5 of 9000 to 20000, 40 heads, 45.7, 32.9, 30.2, 37.5; one of 20000 among 63
+  // of 300, 32 heads, 39.1, 25.9, 33.7, 85; 64 of 511 to 4096, 128 heads, 75.7, 83, 127, 357.)
+  const long long heads = (long long)a.Hq * a.B;
+  if (p.G >= 64 * a.B && most_tiles >= 128 && heads * p.nm <= 4LL * a.sms) {
     cfg.blockDim = dim3(512);
     cfg.gridDim = dim3(a.Hq * p.nm, a.B);
-    return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<16>, a, p.NH, p.groups, p.G);
+    return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<16, 1>, a, p.NH, p.groups, p.G);
   }
+  if (p.G > 8 * a.B && heads * p.nm <= 8LL * a.sms) {
+    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(a.Hq * p.nm, a.B);
+    return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<4, 1>, a, p.NH, p.groups, p.G);
+  }
+  if (heads <= 16LL * a.sms) {
+    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(a.Hq, a.B);
+    return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<4, 4>, a, p.NH, p.groups, p.G);
+  }
+  cfg.blockDim = dim3(256);
   cfg.gridDim = dim3((a.Hq + 7) / 8, a.B);
-  return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<1>, a, p.NH, p.groups, p.G);
+  return cudaLaunchKernelEx(&cfg, stief_shared_merge_kernel<1, 4>, a, p.NH, p.groups, p.G);
 }
 
 }  // namespace stief

@@ -192,3 +192,16 @@ def test_expand_more_rows_than_room_and_unmapped():
     table[1, 0] = -3
     k, v, _ = _expand(pool.to(DEV), table.to(DEV), _i([0, 100, 190]), W, W, 190, 0)
     assert torch.all(k[100:164] == 0) and torch.all(v[100:164] == 0) and torch.equal(k[164:], full[0][164:])
+
+
+@pytest.mark.parametrize("lens,Hq,r,dr", [
+    ([9100], 24, 512, 64), ([8300, 0], 5, 256, 0),                                    # very many parts
+    ([2000, 3000, 1, 700], 48, 512, 64), ([1500, 0, 900], 128, 96, 32),               # four warps, 128 dims each
+    ([64] * 20 + [6000] + [300] * 19, 32, 512, 64), ([500] * 30 + [9000], 16, 192, 16),  # four warps, all dims
+    ([10] * 20 + [7000, 0] + [257] * 20, 128, 384, 0)])                               # a warp a head
+def test_decode_many_parts(lens, Hq, r, dr):
+    q, pool, table = _case(lens, Hq, r, dr, 64, sum(lens) + Hq)
+    scale = 1.5 / (r + dr) ** 0.5
+    got = _decode(q, pool, table, lens, r, scale)
+    check(got, *_want(q, pool, table, lens, r, scale))
+    assert torch.equal(got, _decode(q, pool, table, lens, r, scale))
