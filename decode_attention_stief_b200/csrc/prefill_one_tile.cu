@@ -148,8 +148,9 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
   const long long most = (long long)last + n_all - nq + 1;
   int n = most > 0 ? (int)((min(most, (long long)n_all) + kKeys - 1) / kKeys) : 0;
   int n_k = n_all, before = 0;  // keys from k0 on, and those of the CTAs before this one
+  const int per = kSplit ? (n + p.split - 1) / p.split : n;  // steps of a CTA
   if (kSplit) {
-    const int per = (n + p.split - 1) / p.split, js = min(n, rank * per);
+    const int js = min(n, rank * per);
     n = min(per, n - js);
     before = js * kKeys;
     k0 += before;
@@ -443,14 +444,17 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
           ml[k] = load_cluster_f2(at + kPartMl + (uint32_t)r * 8);
           o[k] = load_cluster_f4(at + (uint32_t)r * kPartRow + (uint32_t)((lane ^ (r & 31)) << 4));
         }
+      // A part counts if the row sees a key of it, whatever its sum: a NaN must reach the row, and a row
+      // whose scores are all -inf is 0 / 0, as in a tile that is not split.
+      const int sees = (int)max(0LL, min((long long)n_all, (long long)query + n_all - nq + 1));
       float top = kFloor, l = 0.f;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kMaxSplit; ++k)
-        if (k < p.split && ml[k].y > 0.f) top = fmaxf(top, ml[k].x);
+        if (k < p.split && k * per * kKeys < sees) top = fmaxf(top, ml[k].x);
 #pragma unroll
       for (int k = 0; k < kMaxSplit; ++k)
-        if (k < p.split && ml[k].y > 0.f) {
+        if (k < p.split && k * per * kKeys < sees) {
           const float f = fast_exp2(ml[k].x - top);
           l += f * ml[k].y;
           x.x += f * o[k].x;
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
           x.z += f * o[k].z;
           x.w += f * o[k].w;
         }
-      const float inv = l > 0.f ? 1.f / l : 0.f;  // (zeros for a row that sees no key)
+      const float inv = sees > 0 ? 1.f / l : 0.f;  // (zeros for a row that sees no key)
       *reinterpret_cast<uint2*>(a.out + ((size_t)(q0 + query) * a.Hq + h) * 128 + lane * 4) =
           make_uint2(pack_bf16x2_rn(x.x * inv, x.y * inv), pack_bf16x2_rn(x.z * inv, x.w * inv));
     }
