@@ -31,6 +31,7 @@ STATUS = {
 DEV_CAPACITY_OVERFLOW = 0x1
 DEV_WAIT_TIMEOUT = 0x2
 DEV_BAD_LENGTH = 0x4
+DEV_TMEM_PAIR = 0x10
 
 
 class StiefError(RuntimeError):

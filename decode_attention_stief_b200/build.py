@@ -6,8 +6,8 @@ statically so the library loads beside any torch build.
 
 ``build_library(variant="testhooks")`` builds ``libstief_testhooks.so`` from the
 same sources with ``-DSTIEF_TEST_HOOKS``: bounded waits that give up after 50 ms
-and two test-only exports (a setup-barrier stall that makes the waits run out,
-the address of the no-allocation scratch).  Only the timeout tests load it.
+and three test-only exports (a setup-barrier stall that makes the waits run out,
+a mismatch of a CTA pair's tensor memory, the address of the no-allocation scratch).  Only the timeout tests load it.
 
 ``build_marshal()`` builds ``_marshal.so`` with g++: a CPython extension that takes
 torch tensors to the library's calls without the cost of doing so in Python.  The

@@ -122,13 +122,14 @@ DevInfo g_dev_info[kMaxDevices];
 std::once_flag g_dev_once[kMaxDevices];
 
 #ifdef STIEF_TEST_HOOKS
-std::atomic<uint32_t> g_test_stall{0};
+std::atomic<uint32_t> g_test_stall{0}, g_test_apart{0};
 #endif
 
 }  // namespace
 
 #ifdef STIEF_TEST_HOOKS
 uint32_t test_stall_bytes() { return g_test_stall.load(); }
+uint32_t test_tmem_apart() { return g_test_apart.load(); }
 #endif
 
 namespace {
@@ -304,4 +305,8 @@ stief_status plan_decode(DecodeArgs& a, const uint16_t* q, const uint16_t* P_K,
 // each CTA's (half's) first copy, so their bounded waits run out (0 turns it off).  The bytes
 // must be a multiple of 16.
 extern "C" STIEF_API void stief_test_set_stall(uint32_t bytes) { stief::g_test_stall.store(bytes); }
+
+// Test build only: the paired prompt CTAs launched after this call take their tensor memory to lie
+// `columns` apart, as if the two allocations had not matched (0: off).
+extern "C" STIEF_API void stief_test_set_tmem_apart(uint32_t columns) { stief::g_test_apart.store(columns); }
 #endif

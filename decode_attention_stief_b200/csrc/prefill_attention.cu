@@ -63,6 +63,7 @@ struct Args {
   int negate;       // scale < 0: the products are negated instead
 #ifdef STIEF_TEST_HOOKS
   uint32_t stall;   // test build: bytes expected of the first copy that none delivers
+  uint32_t apart;   // test build: the pair's tensor memory is taken not to match
 #endif
 };
 
@@ -97,9 +98,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2) stief_p
   uint64_t* drain = s_full + 10;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 11);
 #ifdef STIEF_TEST_HOOKS
-  const uint32_t stall = p.stall;
+  const uint32_t stall = p.stall, apart = p.apart;
 #else
-  constexpr uint32_t stall = 0u;
+  constexpr uint32_t stall = 0u, apart = 0u;
 #endif
   if ((smem_u32(smem) & 1023u) != 0) {
     if (tid == 0) report(a.dev_status, STIEF_DEV_SMEM_ALIGN);
@@ -148,9 +149,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2) stief_p
   cluster_sync();  // both CTAs have their barriers and their tensor memory
   pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
-  // (a product takes both CTAs' operands and results from the same columns)
-  if (load_cluster(in_cta(tmem_slot, rank ^ 1u)) != tmem) {
-    if (tid == 0) report(a.dev_status, STIEF_DEV_WAIT_TIMEOUT);
+  // A product takes both CTAs' operands and results from the same columns.  The two allocate together,
+  // and with other kernels' CTAs on one of the two SMs their columns have not been seen to differ, but
+  // nothing documented promises it: if they do, nothing is computed and no row is written.
+  const bool paired = load_cluster(in_cta(tmem_slot, rank ^ 1u)) == tmem + apart;
+  if (!paired) {
+    if (tid == 0) report(a.dev_status, STIEF_DEV_TMEM_PAIR);
     n = 0;
   }
 
@@ -283,7 +287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2) stief_p
     const uint64_t scale2 = pack2(p.scale2, p.scale2);
     float m = kFloor;
     uint64_t l0 = 0, l1 = 0;
-    bool ok = true;
+    bool ok = paired;
     for (int j = 0; j < n; ++j) {
       ok = __all_sync(~0u, mbar_wait_ready(&s_full[j & 1], (uint32_t)((j >> 1) & 1), a.dev_status));
       if (!ok) break;
@@ -421,6 +425,7 @@ cudaError_t launch_pair(const PrefillArgs& a, int pack, cudaStream_t stream) {
   p.negate = a.scale < 0;
 #ifdef STIEF_TEST_HOOKS
   p.stall = test_stall_bytes();
+  p.apart = test_tmem_apart();
 #endif
   const long long blocks = 2LL * p.qtiles * (a.Hq / p.pack) * a.B;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;

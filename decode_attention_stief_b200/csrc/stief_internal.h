@@ -246,6 +246,8 @@ cudaError_t launch_compress(const CompressArgs& a, cudaStream_t stream);
 #ifdef STIEF_TEST_HOOKS
 // test build only: the stall the next decode launches are planned with (see DecodeArgs)
 uint32_t test_stall_bytes();
+// test build only: columns by which the tensor memory of a pair is taken not to match
+uint32_t test_tmem_apart();
 #endif
 // Joint value latents: keys per head into k_lat, the values of all KV heads of a token
 // through P_V = P_VJ [Hkv*d][rV] into v_lat = v_joint [B][L_max][rV]; then the lengths.

@@ -79,6 +79,9 @@ typedef enum stief_status {
 #define STIEF_DEV_SMEM_ALIGN 0x8u        /* decode: dynamic shared memory was not 1 KiB
                                             aligned as the swizzled key tiles need;
                                             nothing was computed */
+#define STIEF_DEV_TMEM_PAIR 0x10u        /* prompt attention: the two CTAs of a pair were
+                                            given different tensor-memory columns; their
+                                            rows of the output were left as they were */
 
 /*
  * stief_compress_append -- compressed storage of new keys and values
