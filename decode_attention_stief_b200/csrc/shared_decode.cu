@@ -87,8 +87,8 @@ struct Args {
 struct Layout {
   uint32_t stages, p, ml, bars, total;
 };
-__host__ __device__ inline Layout layout_of(int na, int sa, int NH, int nstage) {
-  Layout l;
+__host__ __device__ constexpr Layout layout_of(int na, int sa, int NH, int nstage) {
+  Layout l{};
   l.stages = (uint32_t)na * NH * 128;  // q~ comes first
   l.p = l.stages + (uint32_t)(nstage * sa) * kAtom;
   l.ml = l.p + (uint32_t)NH * 128;
@@ -96,6 +96,11 @@ __host__ __device__ inline Layout layout_of(int na, int sa, int NH, int nstage) 
   l.total = l.bars + 8 * (4 * kMaxStages + 16);
   return l;
 }
+// One CTA an SM (it holds all of the tensor memory).  The smallest ring of eight stages takes 133 KB;
+// with fewer stages another one of at most nine atoms did not fit.
+static_assert(2 * (layout_of(1, 2, 16, kMaxStages).total + 1024) > 228 * 1024 &&
+                  2 * (kMaxSmemPerBlock - 1024 - 9 * kAtom) > 228 * 1024,
+              "two CTAs do not fit an SM");
 
 // Workspace: meta int2 [B] (padded to 256 bytes), (m, l) [slots][kMaxHeads], o~ [slots][NH][r].
 __host__ __device__ inline size_t meta_bytes(int B) { return ((size_t)B * 8 + 255) / 256 * 256; }
@@ -229,10 +234,22 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     prefetch_tensormap(&p.ma);
     prefetch_tensormap(&p.mb);
   }
-  if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
 
+  // Tensor memory only after the dependency wait, and dependents only once it is held: an allocation
+  // waits without a limit, and a CTA that has columns while it waits for another kernel must not
+  // starve one of that kernel's.
   pdl_wait();
-  pdl_launch_dependents();
+  if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
+  auto load_q = [&](int b, uint32_t more) {  // (by one thread)
+    mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128) + more);
+    for (int c = 0; c < p.na; ++c)
+      tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, b * a.Hq + h_base, q_full, l2_policy_evict_last());
+  };
+  int page = 0;
+  if (p.direct && warp == 0 && cta < a.B) {  // the query and the first page wait for no one
+    if (tid == 0) load_q(cta, stall);
+    page = __ldg(a.block_table + (size_t)cta * a.max_pages);
+  }
   int per = 1, count = 0;  // the CTA's share begins at g0 and costs `count`
   long long g0 = 0;
   if (p.direct) {  // a CTA a sequence
@@ -240,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();
     if (count > 0 && group == 0 && tid == 64) {
       const int L = __ldg(a.seq_lens + cta);
       if (valid_length(L, a.max_seq_len) != L) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
@@ -267,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();
     int total = 0;
     for (int i = 0; i < kThreads / 32; ++i) {
       if (i == warp) incl += total;
@@ -314,24 +333,14 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     // ---------------------------------------------------------------- producer
     if (count > 0 && elect_one()) {
       int got[2] = {0, 0};  // tiles of which the piece is requested
-      const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
+      const uint64_t once = l2_policy_evict_first();
       int i = 0, segs = 0;
       Ring ring{p.nstage};
       bool ok = true;
-      auto load_q = [&](int b, int segs) {
-        mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128) + (segs == 0 ? stall : 0u));
-        for (int c = 0; c < p.na; ++c)
-          tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, b * a.Hq + h_base, q_full, keep);
-      };
-      int page = 0;
-      if (p.direct) {  // the query and the first page do not wait for the length
-        page = __ldg(a.block_table + (size_t)cta * a.max_pages);
-        load_q(cta, 0);
-      }
       while (ok && walk.next(seg)) {
         if (segs > 0) ok = mbar_wait_ready(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status);
         if (!ok) break;
-        if (!p.direct) load_q(seg.b, segs);
+        if (!p.direct) load_q(seg.b, segs == 0 ? stall : 0u);
         ++segs;
         const int32_t* entry = a.block_table + (size_t)seg.b * a.max_pages + seg.t0 * kTok / a.page_size;
         int in_page = seg.t0 * kTok % a.page_size;
@@ -860,9 +869,8 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& a, cudaStream_t stream)
   p.whole = p.direct || most_tiles <= kWholeTiles;
   constexpr uint32_t kMost = kMaxSmemPerBlock - 1024;  // the static part, rounded up
   for (p.nstage = kMaxStages; p.nstage > 2 && layout_of(p.na, p.sa, p.NH, p.nstage).total > kMost;) --p.nstage;
-  uint32_t smem = layout_of(p.na, p.sa, p.NH, p.nstage).total;
+  const uint32_t smem = layout_of(p.na, p.sa, p.NH, p.nstage).total;
   if (smem > kMost) return cudaErrorInvalidValue;
-  if (smem < 120u * 1024u) smem = 120u * 1024u;  // one CTA an SM: it holds all of TMEM
   const uint64_t rows = (uint64_t)a.num_pages * a.page_size, pitch = (uint64_t)p.w * 2;
   p.whole_rows = p.w % 64 == 0;
   if (!encode_tiled_bf16_2d(&p.mq, a.q, (uint64_t)p.w, (uint64_t)a.B * a.Hq, pitch, 64, (uint32_t)p.NH,

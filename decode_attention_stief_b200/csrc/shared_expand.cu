@@ -55,14 +55,19 @@ struct Args {
 struct Layout {
   uint32_t b, out, bars, total;
 };
-__host__ __device__ inline Layout layout_of(int chunks, int na, int nb, int out_rows) {
-  Layout l;
+__host__ __device__ constexpr Layout layout_of(int chunks, int na, int nb, int out_rows) {
+  Layout l{};
   l.b = (uint32_t)(na * chunks) * kAtomA;
   l.out = l.b + (uint32_t)nb * kStageB;
   l.bars = l.out + (uint32_t)(8 * out_rows) * 128;
   l.total = l.bars + 8 * (2 * kMaxStages + 12);
   return l;
 }
+// One CTA an SM (it holds all of the tensor memory).  The smallest layout takes 161 KB; with fewer
+// than six weight chunks another one did not fit.
+static_assert(2 * (layout_of(1, 2, kMaxStages, 32).total + 1024) > 228 * 1024 &&
+                  2 * (kMaxSmemPerBlock - 1024 - kStageB) > 228 * 1024,
+              "two CTAs do not fit an SM");
 
 // Rows [s0, s1) of sequence b (none if kv_start is not ascending from 0 within the outputs).
 __device__ __forceinline__ void rows_of(const SharedExpandArgs& a, int b, int& s0, int& s1) {
@@ -175,10 +180,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
     prefetch_tensormap(&p.mk);
     prefetch_tensormap(&p.mv);
   }
-  if (warp == 1) tmem_alloc_pair(&tmem_slot, kTmemCols);
 
+  // (tensor memory only after the dependency wait, and dependents only once it is held, as in
+  // shared_decode.cu)
   pdl_wait();
-  pdl_launch_dependents();
+  if (warp == 1) tmem_alloc_pair(&tmem_slot, kTmemCols);
   // where this CTA's units begin: a prefix sum of the sequences' row tiles
   const int per_thread = (a.B + kThreads - 1) / kThreads, c0 = min(a.B, tid * per_thread), c1 = min(a.B, c0 + per_thread);
   int sum = 0;
@@ -223,6 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) stief_s
   }
   // (also: the barriers of both CTAs are initialised, and both have their tensor memory)
   cluster_sync();
+  pdl_launch_dependents();
   const uint32_t tmem = tmem_slot;
   Walk walk{a, count > 0 ? start_b : 0, count > 0 ? start_j : 0, (int)(u0 - (long long)(tile0 / 2) * a.H), count};
   if (count > 0 && !leader) walk.move(1);
@@ -405,9 +412,8 @@ cudaError_t launch_shared_expand(const SharedExpandArgs& a, cudaStream_t stream)
   // With one row tile in 128 KB the ring is short, and another chunk is worth more than whole stores
   // (128 heads at r 512: 116 us against 123); with two it is not (r 256: 27.0 us against 23.5).
   if (p.na == 1 && p.nb < kMaxStages && layout_of(p.chunks, 1, p.nb + 1, 16).total <= kMost) ++p.nb, p.out_rows = 16;
-  uint32_t smem = layout_of(p.chunks, p.na, p.nb, p.out_rows).total;
+  const uint32_t smem = layout_of(p.chunks, p.na, p.nb, p.out_rows).total;
   if (smem > kMost) return cudaErrorInvalidValue;
-  if (smem < 120u * 1024u) smem = 120u * 1024u;  // one CTA an SM: it holds all of TMEM
   const uint64_t w = (uint64_t)(a.r + a.dr), r = (uint64_t)a.r;
   if (!encode_tiled_bf16_2d(&p.mc, a.pages, w, (uint64_t)a.num_pages * a.page_size, w * 2, 64, 64,
                             CU_TENSOR_MAP_SWIZZLE_128B) ||
