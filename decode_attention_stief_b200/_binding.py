@@ -905,6 +905,14 @@ def _current():
     return torch.cuda.current_device() if torch.cuda.is_available() else -2
 
 
+def _status_here(dev_status, dev):
+    """Pointer of the status word, which must be on device `dev`: its kernels write there."""
+    ptr = _opt_status(dev_status)
+    if ptr is not None and dev_status.get_device() != dev:
+        raise ValueError(f"dev_status must be on the current device (cuda:{dev}), got {dev_status.device}")
+    return ptr
+
+
 def _ws(workspace, dev):
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
@@ -940,6 +948,7 @@ def stief_plan_pages(new_tokens, seq_lens, block_table, free_pages, free_count, 
             _check("stief_plan_pages", code)
             return
     dev, i32 = _current(), torch.int32
+    status = _status_here(dev_status, dev)
     pn, pl = _here(new_tokens, "new_tokens", i32, 1, dev), _here(seq_lens, "seq_lens", i32, 1, dev)
     pt, pf = _here(block_table, "block_table", i32, 2, dev), _here(free_pages, "free_pages", i32, 1, dev)
     pc, po = _here(free_count, "free_count", i32, 1, dev), _here(free_count_out, "free_count_out", i32, 1, dev)
@@ -961,7 +970,7 @@ def stief_plan_pages(new_tokens, seq_lens, block_table, free_pages, free_count, 
     pw, nw = _ws(workspace, dev)
     _invoke("stief_plan_pages", (pn, pl, pt, pf, pc, ps, pq, pk, pso, po, pw, nw, B,
                                  free_pages.shape[0], int(page_size), max_pages, max_tokens,
-                                 _opt_status(dev_status), _stream_on(stream, dev)))
+                                 status, _stream_on(stream, dev)))
 
 
 def _rows(t, name, dev):
@@ -995,6 +1004,7 @@ def stief_append_shared_paged(c_new, pe_new, slots, pages,
             _check("stief_append_shared_paged", code)
             return
     dev = _current()
+    status = _status_here(dev_status, dev)
     pc, N, r, sc = _rows(c_new, "c_new", dev)
     pp, n_pe, dr, sp = (None, N, 0, 0) if pe_new is None else _rows(pe_new, "pe_new", dev)
     psl = _here(slots, "slots", torch.int32, 1, dev)
@@ -1003,7 +1013,7 @@ def stief_append_shared_paged(c_new, pe_new, slots, pages,
     if slots.shape[0] != N or w != r + dr or n_pe != N:
         raise ValueError("stief_append_shared_paged: inconsistent shapes")
     _invoke("stief_append_shared_paged", (pc, pp if dr else None, psl, ppg, N, r, dr, sc, sp, num_pages,
-                                          page_size, _opt_status(dev_status), _stream_on(stream, dev)))
+                                          page_size, status, _stream_on(stream, dev)))
 
 
 def stief_decode_shared_workspace_bytes(B: int, Hq: int, r: int) -> int:
@@ -1034,6 +1044,7 @@ def stief_decode_shared_paged(q, pages, block_table, seq_lens, out, workspace, m
             _check("stief_decode_shared_paged", code)
             return out
     dev, b16, i32 = _current(), torch.bfloat16, torch.int32
+    status = _status_here(dev_status, dev)
     pq, ppg = _here(q, "q", b16, 3, dev), _here(pages, "pages", b16, 3, dev)
     pt, psl = _here(block_table, "block_table", i32, 2, dev), _here(seq_lens, "seq_lens", i32, 1, dev)
     po = _here(out, "out", b16, 3, dev)
@@ -1046,7 +1057,7 @@ def stief_decode_shared_paged(q, pages, block_table, seq_lens, out, workspace, m
     pw, nw = _ws(workspace, dev)
     _invoke("stief_decode_shared_paged", (pq, ppg, pt, psl, po, pw, nw, B, Hq, r, w - r, num_pages,
                                           page_size, max_pages, int(max_seq_len), float(scale),
-                                          _opt_status(dev_status), _stream_on(stream, dev)))
+                                          status, _stream_on(stream, dev)))
     return out
 
 
@@ -1065,6 +1076,7 @@ def stief_expand_shared_paged(pages, block_table, kv_start, W_K, W_V, k, v, k_pe
             _check("stief_expand_shared_paged", code)
             return
     dev, b16, i32 = _current(), torch.bfloat16, torch.int32
+    status = _status_here(dev_status, dev)
     ppg, pt = _here(pages, "pages", b16, 3, dev), _here(block_table, "block_table", i32, 2, dev)
     pst = _here(kv_start, "kv_start", i32, 1, dev)
     pwk, pwv = _here(W_K, "W_K", b16, 3, dev), _here(W_V, "W_V", b16, 3, dev)
@@ -1078,7 +1090,7 @@ def stief_expand_shared_paged(pages, block_table, kv_start, W_K, W_V, k, v, k_pe
             or kv_start.shape[0] != B + 1 or (dr > 0 and (k_pe is None or k_pe.shape != (N, dr))):
         raise ValueError("stief_expand_shared_paged: inconsistent shapes")
     _invoke("stief_expand_shared_paged", (ppg, pt, pst, pwk, pwv, pk, pv, ppe, B, N, H, d, r, dr,
-                                          num_pages, page_size, max_pages, _opt_status(dev_status),
+                                          num_pages, page_size, max_pages, status,
                                           _stream_on(stream, dev)))
 
 
@@ -1097,6 +1109,7 @@ def stief_prefill_attention(q, k, v, q_start, kv_start, out, max_q_len: int, sca
             _check("stief_prefill_attention", code)
             return out
     dev, b16, i32 = _current(), torch.bfloat16, torch.int32
+    status = _status_here(dev_status, dev)
     pq, pk = _here(q, "q", b16, 3, dev), _here(k, "k", b16, 3, dev)
     pv, po = _here(v, "v", b16, 3, dev), _here(out, "out", b16, 3, dev)
     pqs, pks = _here(q_start, "q_start", i32, 1, dev), _here(kv_start, "kv_start", i32, 1, dev)
@@ -1111,6 +1124,6 @@ def stief_prefill_attention(q, k, v, q_start, kv_start, out, max_q_len: int, sca
             or n_pe != Nkv:
         raise ValueError("stief_prefill_attention: inconsistent shapes")
     _invoke("stief_prefill_attention", (pq, pk, pv, ppe if dr else None, pqs, pks, po, B, Hq, Hkv, d, dr,
-                                        Nq, Nkv, int(max_q_len), float(scale), _opt_status(dev_status),
+                                        Nq, Nkv, int(max_q_len), float(scale), status,
                                         _stream_on(stream, dev)))
     return out
