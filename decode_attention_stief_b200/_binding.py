@@ -905,6 +905,21 @@ def _current():
     return torch.cuda.current_device() if torch.cuda.is_available() else -2
 
 
+def _int32(value, name):
+    """The number as an int that the C call's 32 bits hold (ctypes would cut the rest off)."""
+    value = int(value)
+    if not -0x80000000 <= value <= 0x7fffffff:
+        raise ValueError(f"{name} does not fit 32 bits: {value}")
+    return value
+
+
+def _sizes(func, *sizes):
+    """The sizes of tensors, which 32 bits must hold too."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"{func}: a size does not fit 32 bits: {sizes}")
+    return sizes
+
+
 def _status_here(dev_status, dev):
     """Pointer of the status word, which must be on device `dev`: its kernels write there."""
     ptr = _opt_status(dev_status)
@@ -947,6 +962,7 @@ def stief_plan_pages(new_tokens, seq_lens, block_table, free_pages, free_count, 
         if code is not None:
             _check("stief_plan_pages", code)
             return
+    page_size = _int32(page_size, "page_size")
     dev, i32 = _current(), torch.int32
     status = _status_here(dev_status, dev)
     pn, pl = _here(new_tokens, "new_tokens", i32, 1, dev), _here(seq_lens, "seq_lens", i32, 1, dev)
@@ -968,8 +984,8 @@ def stief_plan_pages(new_tokens, seq_lens, block_table, free_pages, free_count, 
     if not ok:
         raise ValueError("stief_plan_pages: inconsistent shapes")
     pw, nw = _ws(workspace, dev)
-    _invoke("stief_plan_pages", (pn, pl, pt, pf, pc, ps, pq, pk, pso, po, pw, nw, B,
-                                 free_pages.shape[0], int(page_size), max_pages, max_tokens,
+    _invoke("stief_plan_pages", (pn, pl, pt, pf, pc, ps, pq, pk, pso, po, pw, nw,
+                                 *_sizes("stief_plan_pages", B, free_pages.shape[0], page_size, max_pages, max_tokens),
                                  status, _stream_on(stream, dev)))
 
 
@@ -1012,6 +1028,7 @@ def stief_append_shared_paged(c_new, pe_new, slots, pages,
     num_pages, page_size, w = pages.shape
     if slots.shape[0] != N or w != r + dr or n_pe != N:
         raise ValueError("stief_append_shared_paged: inconsistent shapes")
+    N, r, dr, num_pages, page_size = _sizes("stief_append_shared_paged", N, r, dr, num_pages, page_size)
     _invoke("stief_append_shared_paged", (pc, pp if dr else None, psl, ppg, N, r, dr, sc, sp, num_pages,
                                           page_size, status, _stream_on(stream, dev)))
 
@@ -1043,6 +1060,7 @@ def stief_decode_shared_paged(q, pages, block_table, seq_lens, out, workspace, m
         if code is not None:
             _check("stief_decode_shared_paged", code)
             return out
+    max_seq_len = _int32(max_seq_len, "max_seq_len")
     dev, b16, i32 = _current(), torch.bfloat16, torch.int32
     status = _status_here(dev_status, dev)
     pq, ppg = _here(q, "q", b16, 3, dev), _here(pages, "pages", b16, 3, dev)
@@ -1055,8 +1073,9 @@ def stief_decode_shared_paged(q, pages, block_table, seq_lens, out, workspace, m
     if wp != w or r > w or Ho != Hq or not Bo == Bt == B == seq_lens.shape[0]:
         raise ValueError("stief_decode_shared_paged: inconsistent shapes")
     pw, nw = _ws(workspace, dev)
-    _invoke("stief_decode_shared_paged", (pq, ppg, pt, psl, po, pw, nw, B, Hq, r, w - r, num_pages,
-                                          page_size, max_pages, int(max_seq_len), float(scale),
+    _invoke("stief_decode_shared_paged", (pq, ppg, pt, psl, po, pw, nw,
+                                          *_sizes("stief_decode_shared_paged", B, Hq, r, w - r, num_pages, page_size,
+                                                  max_pages), max_seq_len, float(scale),
                                           status, _stream_on(stream, dev)))
     return out
 
@@ -1089,9 +1108,9 @@ def stief_expand_shared_paged(pages, block_table, kv_start, W_K, W_V, k, v, k_pe
     if dr < 0 or W_V.shape != W_K.shape or k.shape != (N, H, d) or v.shape != k.shape \
             or kv_start.shape[0] != B + 1 or (dr > 0 and (k_pe is None or k_pe.shape != (N, dr))):
         raise ValueError("stief_expand_shared_paged: inconsistent shapes")
-    _invoke("stief_expand_shared_paged", (ppg, pt, pst, pwk, pwv, pk, pv, ppe, B, N, H, d, r, dr,
-                                          num_pages, page_size, max_pages, status,
-                                          _stream_on(stream, dev)))
+    _invoke("stief_expand_shared_paged", (ppg, pt, pst, pwk, pwv, pk, pv, ppe,
+                                          *_sizes("stief_expand_shared_paged", B, N, H, d, r, dr, num_pages,
+                                                  page_size, max_pages), status, _stream_on(stream, dev)))
 
 
 def stief_prefill_attention(q, k, v, q_start, kv_start, out, max_q_len: int, scale: float,
@@ -1108,6 +1127,7 @@ def stief_prefill_attention(q, k, v, q_start, kv_start, out, max_q_len: int, sca
         if code is not None:
             _check("stief_prefill_attention", code)
             return out
+    max_q_len = _int32(max_q_len, "max_q_len")
     dev, b16, i32 = _current(), torch.bfloat16, torch.int32
     status = _status_here(dev_status, dev)
     pq, pk = _here(q, "q", b16, 3, dev), _here(k, "k", b16, 3, dev)
@@ -1123,7 +1143,7 @@ def stief_prefill_attention(q, k, v, q_start, kv_start, out, max_q_len: int, sca
     if v.shape != k.shape or dq != d + dr or out.shape != (Nq, Hq, d) or kv_start.shape[0] != B + 1 \
             or n_pe != Nkv:
         raise ValueError("stief_prefill_attention: inconsistent shapes")
-    _invoke("stief_prefill_attention", (pq, pk, pv, ppe if dr else None, pqs, pks, po, B, Hq, Hkv, d, dr,
-                                        Nq, Nkv, int(max_q_len), float(scale), status,
-                                        _stream_on(stream, dev)))
+    _invoke("stief_prefill_attention", (pq, pk, pv, ppe if dr else None, pqs, pks, po,
+                                        *_sizes("stief_prefill_attention", B, Hq, Hkv, d, dr, Nq, Nkv), max_q_len,
+                                        float(scale), status, _stream_on(stream, dev)))
     return out
