@@ -99,10 +99,10 @@ stief_status stief_append_shared_paged(const uint16_t* c_new, const uint16_t* pe
   if (!aligned16(c_new) || !aligned16(pages) || !aligned(slots, 4) || c_stride % 8 != 0 ||
       (dr > 0 && (!aligned16(pe_new) || pe_stride % 8 != 0)))
     return STIEF_ERR_ALIGNMENT;
-  int dev = 0, sms = 0;
-  st = device_check(&dev, &sms);
-  if (st != STIEF_OK) return st;
   stief::SharedAppendArgs a{};
+  int sms = 0;
+  st = device_check(&a.device, &sms);
+  if (st != STIEF_OK) return st;
   a.c = c_new;
   a.pe = pe_new;
   a.slots = slots;

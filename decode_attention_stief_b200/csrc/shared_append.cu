@@ -67,8 +67,12 @@ cudaError_t launch_shared_append(const SharedAppendArgs& a, int sms, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, stief_shared_append_kernel<4>, a)
-              : cudaLaunchKernelEx(&cfg, stief_shared_append_kernel<1>, a);
+  const cudaError_t e = many ? cudaLaunchKernelEx(&cfg, stief_shared_append_kernel<4>, a)
+                             : cudaLaunchKernelEx(&cfg, stief_shared_append_kernel<1>, a);
+  // (a pool without position values may be the per-head pool of one KV head: a paged decode that follows
+  // must not request its rows before this kernel has written them)
+  if (e == cudaSuccess) mark_stream_compress(a.device, stream, true);
+  return e;
 }
 
 }  // namespace stief

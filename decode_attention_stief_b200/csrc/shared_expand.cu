@@ -437,7 +437,10 @@ cudaError_t launch_shared_expand(const SharedExpandArgs& a, cudaStream_t stream)
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, stief_shared_expand_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, stief_shared_expand_kernel, p);
+  // (a decode that takes the keys and values for a cache must not request their rows before they are there)
+  if (e == cudaSuccess) mark_stream_compress(a.device, stream, true);
+  return e;
 }
 
 }  // namespace stief

@@ -34,7 +34,7 @@ struct SharedAppendArgs {
   uint16_t* pages;
   uint32_t* dev_status;
   long long ld_c, ld_pe;  // row strides in elements
-  int N, r, dr;
+  int N, r, dr, device;
   long long num_slots;
 };
 cudaError_t launch_shared_append(const SharedAppendArgs& a, int sms, cudaStream_t stream);

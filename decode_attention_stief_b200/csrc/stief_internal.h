@@ -197,7 +197,8 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 
 // Per (device, stream): whether the library's last launch there wrote cache rows that the next
 // decode could request before its dependency wait: a compress (whose length kernel lets its
-// dependent start early) or an int8 fused step.  Those mark their stream; a decode reads and
+// dependent start early), an int8 fused step, a page plan (block-table entries), a shared append or
+// an expansion.  Those mark their stream; a decode reads and
 // clears the mark (it then requests no cache tile before its dependency wait); the joint
 // compress's CUDA-core path, whose kernels do not let dependents start early, clears it.
 // Host only.

@@ -595,6 +595,7 @@ STIEF_API stief_status stief_plan_pages(const int32_t* new_tokens, const int32_t
  *   slots  : int32 [N]; a negative slot skips its row, one past the pool too, with
  *            STIEF_DEV_CAPACITY_OVERFLOW.  Slots must be distinct: the row of a slot given
  *            twice is a mixture.  The pool must not overlap the inputs.
+ * A decode of this library issued next on the stream reads no row before this call is done.
  */
 STIEF_API stief_status stief_append_shared_paged(const uint16_t* c_new, const uint16_t* pe_new,
                               const int32_t* slots, uint16_t* pages, int N, int r, int dr,
