@@ -19,7 +19,9 @@
 // replaces: 8192 tokens, 32 heads, dr 64, 553 us against 540; 8 chunks of 512 over 3012 keys 251
 // against 219; 1 of 2048 over 6048 keys, 16 heads, 114 against 98.  Two threads a row in the softmax,
 // so that twice as many warps hide each other's latencies: within 2 %.)  Without a position part
-// pairs and single tiles are as fast on long prompts, and single tiles faster on short ones.
+// pairs were as fast as single tiles on long prompts (8192 tokens, 32 heads over 8: 456 us both), slower
+// on shorter ones (2500 tokens 66 us against 58) and faster on chunks over many keys (8 of 512 over 3012
+// 216 against 239); that form is not built.
 // The rest is as in prefill_one_tile.cu: S in two buffers of 64 columns, P over its S, O behind them,
 // half of the tensor memory a CTA; packed heads; the reference of the softmax.
 //   warp 0 of each CTA: TMA producer; warp 1 of the first: MMA issuer; warp 2: zeroes the value rows
@@ -27,8 +29,8 @@
 //   row, and the output.
 // CTAs start with the longest tiles of queries; a pair none of whose rows exists ends at once.
 //
-// Measured: 8192 tokens, 32 heads, dr 64: 540 us, 1.27 PFLOP/s; 8 chunks of 512 over 3012 keys: 219
-// us, 0.94.
+// Measured: 8192 tokens, 32 heads, dr 64: 540 us, 1.27 PFLOP/s (630 us, 1.09, in long runs under the
+// power cap); 8 chunks of 512 over 3012 keys: 219 us, 0.94.
 #include <cstdint>
 
 #include "shared_latent.h"
@@ -468,6 +470,9 @@ cudaError_t launch_pair(const PrefillArgs& a, int pack, cudaStream_t stream) {
 //   300 over 3300, 24 heads                  39.0  27.9  35.0  43.0
 //   1500 tokens, 8 heads                     20.7  18.2  22.5  36.5
 //   2 prompts of 500, 8 heads                10.3  11.7  11.6  24.1
+// Below 8 steps a tile is not split, although four CTAs would save 1.3 us in the second row: the steps
+// are a guess from the arrays' sizes, and a split of fewer costs as much as it saves elsewhere.  The
+// worst case known of the rule is 128 queries over 2128 keys, 128 heads: 35 us with two, 34 with one.
 int split_of(const PrefillArgs& a, int pack) {
   const long long queries = kRows / pack, groups = a.Hq / pack;
   // No more tiles than this, and about so many steps in the longest walk: the lengths are on the GPU,

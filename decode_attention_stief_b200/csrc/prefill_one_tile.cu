@@ -18,22 +18,27 @@
 // and one of values: 1 chunk of 128 over 8128 keys, 128 heads, 200 us; this way 182).
 // Where tiles are few and walks long (split_of in prefill_attention.cu), the CTAs of a cluster share a
 // tile's keys: each walks its part, leaves its rows of O, m and l in fp32 in its shared memory, and
-// joins its share of the rows from all of them.  1 query over 8001 keys, 8 heads over 1: 15.5 us
+// joins its share of the rows from all of them (a part counts if the row sees a key of it, so that a NaN
+// reaches the row as in the other forms).  1 query over 8001 keys, 8 heads over 1: 15.5 us
 // against 82; over 32001: 45 against 313; 8 chunks of 17 over 989, 4 heads: 9.2 against 14.9.
 //   warp 0: TMA producer; warp 1: MMA issuer; warp 2: zeroes the value rows past n_k in the last step
 //   (they may hold NaN, and 0 * NaN is NaN); warps 4-7: softmax, a thread a row, and the output.
 // The softmax's reference is the first step's maximum of the row and moves only when a score passes
 // it by more than 2^60 (weights and sums are floating-point numbers: a large weight loses nothing);
-// the warp then rescales its rows of O, once the last product is done.
+// the warp then rescales its rows of O, once the last product is done.  Weights are rounded to bf16 for
+// the second product (the tensor cores take both operands in one type, and a second product with what
+// the rounding leaves would make the products half as many again); the sum l adds them unrounded: with rounded ones
+// the error against 64 bits is 2 % smaller and the time 1 to 3 % larger.
 //
 // What bounds it: shared memory.  A step's products read 64 KB of it (the queries for every 64 keys
 // anew) and its copies write 32: 768 cycles at 128 bytes a cycle, where the products alone would take
 // 512 and the exponentials, 16 a cycle on an SM, another 512 beside them.  Of the some 1900 cycles that
 // a step of both CTAs takes that is 80 %; the tensor cores are busy for 47 % (chunks) of the time.
 // (Pairs of CTAs, each with half of the keys and values, ask less of it: 8 chunks of 512 over 3012 keys
-// 216 us against 239; but 2500 tokens 66 against 58, and 8192, 32 heads over 8, 456 both.)
-// Measured: 8192 tokens, 32 heads over 8: 456 us, 1.21 PFLOP/s; 8 prompts of 65 to 1500: 84.9 us,
-// 0.74 PFLOP/s (its diagonal tiles compute twice what is counted); 5 prompts of up to 64: 5.7 us.
+// 216 us against 239; but 2500 tokens 66 against 58, and 8192, 32 heads over 8, 456 both.  Not built.)
+// Measured: 8192 tokens, 32 heads over 8: 456 us, 1.21 PFLOP/s (535 us in long runs under the power cap);
+// 8 prompts of 65 to 1500: 80 to 85 us, 0.74 PFLOP/s (its diagonal tiles compute twice what is counted);
+// 5 prompts of up to 64: 5.7 us.
 #include <cstdint>
 
 #include "shared_latent.h"

@@ -25,7 +25,9 @@
 // passes it by more than 2^60 (rare: the accumulator is then rescaled in TMEM).  Weights and sums
 // are floating-point numbers, so a large weight loses nothing, and the maximum of a tile, needed
 // only for that test, is off the path from S to P.  Weights are rounded to bf16 once, and the sum
-// l adds the rounded weights, so that a weight's rounding cancels where it dominates.
+// l adds the rounded weights, so that a weight's rounding cancels where it dominates.  (What the
+// rounding leaves, as a second bf16 operand, has no room: at 64 heads and rank 512 + 64 the queries, two
+// tiles and one buffer of weights take 225 of the 227 KB.)
 //
 // Work: the 64-token tiles of all sequences, in order, are dealt out evenly: CTA c takes what lies
 // in [c per, (c + 1) per), so ragged batches and single long sequences fill the GPU alike.  A
@@ -35,10 +37,10 @@
 // Measured (rank 512 + 64, outputs and caches larger than L2): one sequence of 32768 tokens, 32
 // heads: 19.5 us, 1.9 TB/s over the call, of it 8 us at 4.7 TB/s for the rows (the rest is the
 // start, the parts and their joining).  64 ragged sequences of up to 4096 tokens: 45 us at 32
-// heads (3.8 TB/s), 49 at 64, 76 at 128.  There shared memory is what most is asked of: a tile's
+// heads (3.8 TB/s), 49 at 64, 76 to 82 at 128.  There shared memory is what most is asked of: a tile's
 // copies write 72 KB of it and its products read 240, 2500 cycles at 128 bytes a cycle, of the some
 // 4000 that a tile takes with two in turn (64 heads' queries leave room for no third; the tensor
-// cores are 40 % busy).  The way to memory is not: tiles brought into L2 two ahead, 77 us.  Nor is the
+// cores are 45 % busy).  The way to memory is not: tiles brought into L2 two ahead, 77 us.  Nor is the
 // softmax's length: with two warpgroups, half of a tile's tokens each, 77, and rank 96 29.0 for 28.0.
 #include <cstdint>
 

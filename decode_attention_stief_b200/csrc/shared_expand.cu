@@ -21,7 +21,7 @@
 // a page: two copies bring 64 rows each.
 //
 // Measured: 4096 tokens x 32 heads, r 512: 36.8 us, 0.93 PFLOP/s (29 to 33 us where the 67 MB of output
-// stay in L2), the tensor cores busy for 46 %; 128 heads:
+// stay in L2), the tensor cores busy for 59 %; 128 heads:
 // 116 us, 1.19 PFLOP/s; 3 sequences of 33 to 501 tokens, 8 heads, r 96: 7.4 us.
 #include <cstdint>
 
