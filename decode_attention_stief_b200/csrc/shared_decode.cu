@@ -242,16 +242,6 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
   // starve one of that kernel's.
   pdl_wait();
   if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
-  auto load_q = [&](int b, uint32_t more) {  // (by one thread)
-    mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128) + more);
-    for (int c = 0; c < p.na; ++c)
-      tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, b * a.Hq + h_base, q_full, l2_policy_evict_last());
-  };
-  int page = 0;
-  if (p.direct && warp == 0 && cta < a.B) {  // the query and the first page wait for no one
-    if (tid == 0) load_q(cta, stall);
-    page = __ldg(a.block_table + (size_t)cta * a.max_pages);
-  }
   int per = 1, count = 0;  // the CTA's share begins at g0 and costs `count`
   long long g0 = 0;
   if (p.direct) {  // a CTA a sequence
@@ -265,8 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
       if (valid_length(L, a.max_seq_len) != L) report(a.dev_status, STIEF_DEV_BAD_LENGTH);
     }
   } else {
-    // where this CTA's tiles begin: a prefix sum of the sequences' tile counts
-    const int per_thread = (a.B + kThreads - 1) / kThreads, c0 = tid * per_thread, c1 = min(a.B, c0 + per_thread);
+    // where this CTA's tiles begin: a prefix sum of the sequences' tile counts (warp 1, which allocates
+    // meanwhile, has none of them)
+    constexpr int kCounting = kThreads - 32;
+    const int per_thread = (a.B + kCounting - 1) / kCounting, c0 = (warp > 1 ? tid - 32 : tid) * per_thread;
+    const int c1 = warp == 1 ? c0 : min(a.B, c0 + per_thread);
     auto cost_of = [&](int b) {
       const int n = tiles_of(valid_length(__ldg(a.seq_lens + b), a.max_seq_len));
       return n > 0 ? n + kSegment : 0;
@@ -335,14 +328,24 @@ __global__ void __launch_bounds__(kThreads, 1) stief_shared_decode_kernel(const 
     // ---------------------------------------------------------------- producer
     if (count > 0 && elect_one()) {
       int got[2] = {0, 0};  // tiles of which the piece is requested
-      const uint64_t once = l2_policy_evict_first();
+      const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
       int i = 0, segs = 0;
       Ring ring{p.nstage};
       bool ok = true;
+      auto load_q = [&](int b, int segs) {
+        mbar_arrive_expect_tx(q_full, (uint32_t)(p.na * p.NH * 128) + (segs == 0 ? stall : 0u));
+        for (int c = 0; c < p.na; ++c)
+          tma_load_2d(smem + c * p.NH * 128, &p.mq, 64 * c, b * a.Hq + h_base, q_full, keep);
+      };
+      int page = 0;
+      if (p.direct) {  // the query and the first page do not wait for the length
+        page = __ldg(a.block_table + (size_t)cta * a.max_pages);
+        load_q(cta, 0);
+      }
       while (ok && walk.next(seg)) {
         if (segs > 0) ok = mbar_wait_ready(q_empty, (uint32_t)((segs - 1) & 1), a.dev_status);
         if (!ok) break;
-        if (!p.direct) load_q(seg.b, segs == 0 ? stall : 0u);
+        if (!p.direct) load_q(seg.b, segs);
         ++segs;
         const int32_t* entry = a.block_table + (size_t)seg.b * a.max_pages + seg.t0 * kTok / a.page_size;
         int in_page = seg.t0 * kTok % a.page_size;
