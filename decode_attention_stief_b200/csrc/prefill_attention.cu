@@ -33,6 +33,7 @@
 // power cap); 8 chunks of 512 over 3012 keys: 219 us, 0.94.
 #include <cstdint>
 
+#include "prefill_row.cuh"
 #include "shared_latent.h"
 #include "stief_device.cuh"
 #include "umma.cuh"
@@ -159,6 +160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2) stief_p
     if (tid == 0) report(a.dev_status, STIEF_DEV_TMEM_PAIR);
     n = 0;
   }
+  uint32_t nan = 0, which = 0;  // NaN among a row's outputs, and the warp's rows with one
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -391,6 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2) stief_p
             x.z = pack_bf16x2_rn(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
             x.w = pack_bf16x2_rn(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
           }
+          nan = nan_of(x.x, x.y, nan_of(x.z, x.w, nan));
           *reinterpret_cast<uint4*>(stage + lane * 256 + ((((c + e) >> 3) ^ (lane & 15)) << 4)) = x;
         }
       }
@@ -402,6 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2) stief_p
         const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 256 + ((piece ^ (r & 15)) << 4));
         if (qr < nq) *reinterpret_cast<uint4*>(a.out + ((size_t)(q0 + qr) * a.Hq + h) * 128 + piece * 8) = x;
       }
+      which = __ballot_sync(~0u, has_nan(nan));
     }
   }
   __syncwarp();
@@ -410,6 +414,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2) stief_p
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
+  }
+  if (__builtin_expect(which != 0, 0)) {
+    __syncwarp();
+    redo_rows(a, p.shift, p.qtiles, blockIdx.x / 2, 2 * kRows, kKeys, (int)rank * kRows + (warp & 3) * 32, 1, which,
+              p.negate ? -p.scale2 : p.scale2);
   }
 }
 

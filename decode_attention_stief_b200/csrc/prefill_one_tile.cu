@@ -41,6 +41,7 @@
 // 5 prompts of up to 64: 5.7 us.
 #include <cstdint>
 
+#include "prefill_row.cuh"
 #include "shared_latent.h"
 #include "stief_device.cuh"
 #include "umma.cuh"
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
   tc_fence_after();
   pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
+  uint32_t nan = 0, which = 0;  // NaN among a row's outputs, and the warp's rows with one
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -413,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
             x.z = pack_bf16x2_rn(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
             x.w = pack_bf16x2_rn(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
           }
+          nan = nan_of(x.x, x.y, nan_of(x.z, x.w, nan));
           *reinterpret_cast<uint4*>(stage + lane * 256 + ((((c + e) >> 3) ^ (lane & 15)) << 4)) = x;
         }
       }
@@ -424,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
         const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 256 + ((piece ^ (r & 15)) << 4));
         if (qr < nq) *reinterpret_cast<uint4*>(a.out + ((size_t)(q0 + qr) * a.Hq + h) * 128 + piece * 8) = x;
       }
+      which = __ballot_sync(~0u, has_nan(nan));
     }
   }
   __syncwarp();
@@ -468,11 +472,18 @@ __global__ void __launch_bounds__(kThreads, 2) stief_prefill_one_tile_kernel(con
           x.w += f * o[k].w;
         }
       const float inv = sees > 0 ? 1.f / l : 0.f;  // (zeros for a row that sees no key)
-      *reinterpret_cast<uint2*>(a.out + ((size_t)(q0 + query) * a.Hq + h) * 128 + lane * 4) =
-          make_uint2(pack_bf16x2_rn(x.x * inv, x.y * inv), pack_bf16x2_rn(x.z * inv, x.w * inv));
+      const uint2 y = make_uint2(pack_bf16x2_rn(x.x * inv, x.y * inv), pack_bf16x2_rn(x.z * inv, x.w * inv));
+      *reinterpret_cast<uint2*>(a.out + ((size_t)(q0 + query) * a.Hq + h) * 128 + lane * 4) = y;
+      if (__any_sync(~0u, has_nan(nan_of(y.x, y.y, 0)))) which |= 1u << (i / (kThreads / 32));
     }
     __syncwarp();
     cluster_sync();  // no part is read any more
+  }
+  if (__builtin_expect(which != 0, 0)) {
+    __syncwarp();
+    const int first_row = kSplit ? rank * (kRows / p.split) + warp : (warp & 3) * 32;
+    redo_rows(a, p.shift, p.qtiles, tile, kRows, kKeys, first_row, kSplit ? kThreads / 32 : 1, which,
+              p.negate ? -p.scale2 : p.scale2);
   }
 }
 

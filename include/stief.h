@@ -660,9 +660,9 @@ STIEF_API stief_status stief_expand_shared_paged(const uint16_t* pages, const in
  * without a launch (no length is looked at).  max_q_len sizes the grid: give the longest chunk's
  * length, as a CTA is launched for each tile up to it in every sequence (8 prompts of up to 1500
  * tokens: 82 us, 150 with a limit of 8192).  The weights enter the second product rounded
- * to bf16.  Rows of no sequence, or of another one, may hold anything; a value row of the sequence
- * itself that is not finite may also reach queries of the same sequence that do not see it (as a
- * weight of 0).
+ * to bf16.  Rows of no sequence, of another one, or of keys that a query does not see may hold
+ * anything (rows that a NaN or an infinity among the latter would have reached are computed anew, one
+ * at a time: slower, and only those).  out must not overlap the inputs.
  */
 STIEF_API stief_status stief_prefill_attention(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                               const uint16_t* k_pe, const int32_t* q_start, const int32_t* kv_start,
