@@ -3,13 +3,18 @@
 //
 // The second product adds P . V over all keys of a step, with weights of 0 for the keys that a row does
 // not see; where such a key's value is NaN or infinite, 0 times it is NaN.  Such a row is known by a NaN
-// in its output and computed anew over the keys it sees, a warp a row: a lane scores a key of 32, then
-// all lanes add the 32 values, four dimensions each.  (Making the values of the diagonal's steps finite
-// before their product would cost every call a look at them.)  All of it happens after the tile's
-// work, from the arguments alone, so that the kernels keep no more than a bit a row for it, and in loops that
-// are not unrolled: calls without a NaN take 0.1 us longer (77 tokens 6.28 -> 6.38 us, 8 prompts of 65 to 1500
-// and 8192 tokens within 1 %; as a function that is called, 1 to 4 % longer).  The walk ends once every
-// element in question is NaN: a tensor full of NaN costs a step of 32 keys a row.
+// in its output and computed anew, a warp a row, backwards over the keys of the tile's steps: first the
+// unseen ones, which say in which dimensions the NaN may be theirs, then those it sees.  A lane scores a
+// key of 32, then all lanes add the 32 values, four dimensions each.  The walk ends once no element is in
+// question, or every one is NaN by a key that is seen.
+//
+// (Making the values of the diagonal's steps finite before their product would cost every call a look at
+// them.)  All of it happens after the tile's work, from the arguments alone, so that the kernels keep no more
+// than a bit a row for it: calls without a NaN take 0.1 us longer (77 tokens 6.28 -> 6.38 us, 8 prompts of 65 to
+// 1500 and 8192 tokens as before).  That hangs on this form: called as a function, with a loop of its own over
+// the unseen values, or with more loads in flight, it cost the kernels' main loops 2 to 5 %.  Bound by the
+// latency of the rows' loads; 8192 tokens, 32 heads, position part: 0.54 ms without a NaN, 4.5 with one token
+// of NaN in the middle, 5.6 with NaN from there on, 9.8 with nothing else.
 #pragma once
 
 #include "shared_latent.h"
@@ -34,9 +39,11 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y, float s) {
   return s;
 }
 
-// The NaN elements of the output of query row `qr` and head `h`, over keys [k0, k0 + seen) of KV head
-// `hk`.  scale2: scale * log2(e), with its sign.  All lanes of a warp.
-__device__ __forceinline__ void redo_row(const PrefillArgs& a, int qr, int h, int hk, int k0, int seen, float scale2) {
+// The NaN elements of the output of query row `qr` and head `h` that a value of keys [k0 + seen, k0 + walked)
+// may have made, over keys [k0, k0 + seen) of KV head `hk`.  scale2: scale * log2(e), with its sign.  All
+// lanes of a warp.
+__device__ __forceinline__ void redo_row(const PrefillArgs& a, int qr, int h, int hk, int k0, int seen, int walked,
+                                         float scale2) {
   const int lane = threadIdx.x & 31;
   uint2* at = reinterpret_cast<uint2*>(a.out + ((size_t)qr * a.Hq + h) * 128) + lane;
   const uint2 old = *at;
@@ -47,14 +54,15 @@ __device__ __forceinline__ void redo_row(const PrefillArgs& a, int qr, int h, in
   if (!__any_sync(~0u, any)) return;
   const uint4* q = reinterpret_cast<const uint4*>(a.q + ((size_t)qr * a.Hq + h) * (128 + a.dr));
   float m = -1e30f, l = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f}, far[4] = {0.f, 0.f, 0.f, 0.f};  // far: of values not finite
+  uint32_t unseen = 0;  // elements with an unseen value that is not finite
 #pragma unroll 1
-  for (int j0 = 0; j0 < seen; j0 += 32) {
+  for (int j0 = (walked - 1) / 32 * 32; j0 >= 0; j0 -= 32) {
     float s = -INFINITY;
     if (j0 + lane < seen) {
       const size_t row = (size_t)k0 + j0 + lane;
       const uint4* k = reinterpret_cast<const uint4*>(a.k + (row * a.Hkv + hk) * 128);
       float y = 0.f;
-#pragma unroll 1
+#pragma unroll 4
       for (int c = 0; c < 16; ++c) y = dot8(__ldg(q + c), __ldg(k + c), y);
       const uint4* pe = reinterpret_cast<const uint4*>(a.pe + row * a.dr);
 #pragma unroll 1
@@ -70,19 +78,29 @@ __device__ __forceinline__ void redo_row(const PrefillArgs& a, int qr, int h, in
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] *= f;
 #pragma unroll 1
-    for (int t = 0; t < min(32, seen - j0); ++t) {
-      const float w = __shfl_sync(~0u, p, t);
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.v + (((size_t)k0 + j0 + t) * a.Hkv + hk) * 128) + lane);
-      const float y[4] = {bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y)};
+    for (int t0 = 0; t0 < min(32, walked - j0); t0 += 8) {
+      uint2 v[8];  // (loads in flight together: the walk is bound by their latency)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (isfinite(y[e])) sum[e] = fmaf(w, y[e], sum[e]);
-        else far[e] += w * y[e];
+      for (int t = 0; t < 8; ++t)
+        v[t] = __ldg(reinterpret_cast<const uint2*>(a.v + (((size_t)k0 + min(j0 + t0 + t, walked - 1)) * a.Hkv + hk) * 128) + lane);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float w = __shfl_sync(~0u, p, t0 + t);
+        const float y[4] = {bf16lo(v[t].x), bf16hi(v[t].x), bf16lo(v[t].y), bf16hi(v[t].y)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (isfinite(y[e])) sum[e] = fmaf(w, y[e], sum[e]);
+          else if (j0 + t0 + t < seen) far[e] += w * y[e];
+          else unseen |= 1u << e;
+        }
       }
     }
     bool done = true;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) done &= !odd[e] || isnan(far[e]) || isnan(sum[e]);
+    for (int e = 0; e < 4; ++e) {
+      if (j0 <= seen) odd[e] = odd[e] && (unseen >> e & 1u);  // (every unseen value has been looked at)
+      done &= !odd[e] || isnan(far[e]) || isnan(sum[e]);
+    }
     if (__all_sync(~0u, done)) break;
   }
 #pragma unroll 1
@@ -110,7 +128,7 @@ __device__ __forceinline__ void redo_rows(const PrefillArgs& a, int shift, int q
     const int row = first_row + (__ffs(which) - 1) * step, query = begin + (row >> shift);
     const int seen = (int)max(0LL, min((long long)n_k, (long long)query + n_k - nq + 1));
     if (query < nq && seen > 0 && seen < walked)
-      redo_row(a, q0 + query, h0 + (row & ((1 << shift) - 1)), hk, k0, seen, scale2);
+      redo_row(a, q0 + query, h0 + (row & ((1 << shift) - 1)), hk, k0, seen, walked, scale2);
   }
 }
 
